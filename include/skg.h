@@ -271,6 +271,185 @@ skg_status skg_gemm_tiled(skg_fmt fmt, int64_t M, int64_t K, int64_t N, const vo
                           float* y, hipStream_t stream);
 
 /*
+ * Between the QKV product and the output projection
+ * =================================================
+ *
+ * The products above leave a decode layer's queries, keys and values as
+ * float32 rows, [T][heads][head_dim] for T tokens.  The entry points below
+ * normalise and rotate them, keep keys and values in a paged cache of 16, 8
+ * or 4 bits, and attend from the tokens to that cache; the last of them can
+ * write the Q8_1 blocks that the output projection's product reads.
+ *
+ * Element types of rows, and formats of a cache.
+ */
+typedef enum skg_dtype { SKG_F32 = 0, SKG_BF16 = 1 } skg_dtype;
+
+typedef enum skg_kv_fmt {
+  SKG_KV_BF16 = 0, /* bf16                                                   */
+  SKG_KV_Q8_0 = 1, /* 32-element blocks: fp16 d, codes of 8 bits, d * q      */
+  SKG_KV_Q4_0 = 2  /* 32-element blocks: fp16 d, codes of 4 bits, d * (c - 8) */
+} skg_kv_fmt;
+
+/*
+ * A paged cache of keys and values.  It is the caller's: two device buffers
+ * of skg_kv_bytes(...) bytes each, 16-byte aligned, and this description,
+ * which is read during a call only.
+ *
+ * Slot s (0 <= s < pages * page_size) is token s % page_size of page
+ * s / page_size.  A buffer is [pages][heads][chunk]; a chunk holds the codes
+ * of the page's tokens, [page_size][row bytes], then for q8_0 and q4_0 their
+ * scales, fp16 [page_size][head_dim / 32].  With NB = head_dim / 32, c < 16,
+ * b < NB, e < 2, a row's element 32 b + 2 c + e is
+ *   bf16 : uint16 32 b + 2 c + e (in order)      row bytes 2 head_dim
+ *   q8_0 : byte 2 NB c + 2 b + e, holding q + 128    row bytes head_dim
+ *   q4_0 : byte NB c + b, nibble e (low first), holding the code
+ *                                                row bytes head_dim / 2
+ * so that 2 NB consecutive elements of a row hold two of every block: the
+ * matrix-core operand of one block is then whole bytes of each lane, and a
+ * block's scale multiplies one operand instead of single products.
+ *
+ * heads 1..65535; head_dim 64, 128 or 256; page_size a power of two in
+ * 16..2^20; pages 1..2^31 - 1.
+ */
+typedef struct skg_kv_cache {
+  int32_t fmt; /* skg_kv_fmt */
+  int32_t heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int64_t pages;
+  void* k;
+  void* v;
+} skg_kv_cache;
+
+/* Bytes of one of a cache's two buffers, or 0 if the description is invalid. */
+size_t skg_kv_bytes(skg_kv_fmt fmt, int heads, int head_dim, int page_size, int64_t pages);
+
+/*
+ * Normalisation and rotation of queries and keys, head by head, in one pass.
+ *
+ * Per row x[head_dim] of a token at position p, in binary32:
+ *   norm != 0 : x = x * r * g, r = 1 / sqrt(sum x^2 / head_dim + eps); g is gq
+ *               for queries and gk for keys, float32 [head_dim], 16-byte
+ *               aligned, or NULL for a gain of 1 (norm == 0 reads neither).
+ *   rotation  : with th_i = p * inv_freq[i], i < rot / 2, formed and reduced
+ *               in binary64, the pair (a, b) becomes
+ *               (a cos th - b sin th, a sin th + b cos th); it is
+ *               (x[2i], x[2i + 1]) if interleaved, else (x[i], x[i + rot/2]).
+ *               Elements from rot on are not turned.
+ * rot: multiple of 16 in 0..head_dim; with 0, pos and inv_freq may be NULL.
+ * pos: int32 [T], any value.  inv_freq: float32 [rot / 2].
+ * eps: finite, >= 0; with eps == 0 an all-zero row has no normalisation.
+ */
+typedef struct skg_rope {
+  int32_t rot;
+  int32_t interleaved;
+  int32_t norm;
+  float eps;
+  const int32_t* pos;
+  const float* inv_freq;
+  const float* gq;
+  const float* gk;
+} skg_rope;
+
+/*
+ * skg_qk_norm_rope: q and k are rows of `dtype` ([T] tokens, ldq / ldk elements
+ * apart, of hq / hk heads of head_dim), qo and ko the results in the same type,
+ * rounded once.  hq or hk may be 0 (then its pointers are not read).  q == qo
+ * with ldq == ldqo (and k likewise) works in place; any other overlap of an
+ * input with an output, or of the outputs, is refused.  Row pointers are 16-byte aligned and row
+ * strides a multiple of 16 bytes, at least heads * head_dim elements (T > 1).
+ * 1 <= T <= 2^24; head_dim 64, 128 or 256; hq + hk in 1..65535.
+ * Errors: SKG_E_SHAPE (T, heads, head_dim, rot, strides), SKG_E_INVALID_ARG
+ * (null pointers, unknown dtype, eps, overlaps), SKG_E_ALIGN.
+ */
+skg_status skg_qk_norm_rope(skg_dtype dtype, int64_t T, int hq, int hk, int head_dim, const void* q, int64_t ldq,
+                            const void* k, int64_t ldk, const skg_rope* rope, void* qo, int64_t ldqo, void* ko,
+                            int64_t ldko, hipStream_t stream);
+
+/*
+ * skg_kv_store: encodes T tokens' keys and values (rows of `dtype`, ldk / ldv
+ * elements apart, cache->heads heads) into slots[t] (int64, device) of the
+ * cache.  A slot outside the cache (negative, for padding, or too large) is
+ * skipped.  Slots of one call are distinct: a slot that is named twice holds
+ * bytes of both tokens.  Bytes of other slots are not touched.
+ * bf16 rows are rounded to nearest even.  q8_0, per 32-element block in
+ * binary32: d = max|x| / 127, q = round-half-away(x * (1 / d)), 0 if d is 0;
+ * q4_0: m the element of largest magnitude (the first of equals), d = m / -8,
+ * code = round-half-away(x * (1 / d)) + 8 in 0..15, 8 if d is 0; d is stored
+ * in fp16, nearest even, at most 65504 in magnitude.  A block with an
+ * infinite or NaN element is outside the domain of q8_0 and q4_0: it is
+ * stored as some finite values.
+ *
+ * skg_kv_load: the values in slots[t], d * q exactly in binary32, rounded once
+ * to bf16 for that type, to rows of k and v.  Rows of slots outside the cache
+ * become 0; a slot may be named many times.
+ *
+ * skg_qkv_rope_store: skg_qk_norm_rope of q to qo, and skg_kv_store of the
+ * normalised and rotated k (the binary32 values, before any rounding to bf16)
+ * and of v, in one launch.  q, k, v have the same type; the heads of k and v
+ * are the cache's.
+ *
+ * 1 <= T <= 2^24.  Row alignment and strides as above.
+ */
+skg_status skg_kv_store(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, const void* k, int64_t ldk,
+                        const void* v, int64_t ldv, const int64_t* slots, hipStream_t stream);
+skg_status skg_kv_load(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, const int64_t* slots, void* k,
+                       int64_t ldk, void* v, int64_t ldv, hipStream_t stream);
+skg_status skg_qkv_rope_store(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, int hq, const void* q,
+                              int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                              const skg_rope* rope, const int64_t* slots, void* qo, int64_t ldqo,
+                              hipStream_t stream);
+
+/*
+ * Attention of drafted tokens over a cache: n_seqs sequences, each with a
+ * context and a tree (or a chain, or one) of at most 64 drafted tokens whose
+ * keys and values are in the cache already.
+ *
+ * Sequence b has tokens cu[b] .. cu[b+1]-1 of q (cu: int32 [n_seqs + 1], never
+ * falling, in 0..T; NULL gives every sequence T / n_seqs tokens, which must be
+ * whole) and a context of ctx[b] >= 0 keys.  Its key j lies in slot
+ * table[b][j / page_size] * page_size + j % page_size (table: int32
+ * [n_seqs][width]); drafted token i is key ctx[b] + i.  Token i sees the
+ * context and the drafted tokens j of its sequence with bit j of its mask set
+ * (mask: uint64 [T]; NULL is a chain, j <= i).
+ *   s_j = scale * <q, k_j>,  o = sum_j e^(s_j - max s) v_j / sum_j e^(s_j - max s)
+ * over the keys that it sees; a token that sees none gets 0.  Keys on a page
+ * outside the cache or past the table's width are not there.  Query head h
+ * reads cache head h / (hq / heads).
+ *
+ * A sequence's tokens past the max_draft-th are neither computed nor seen, and
+ * neither their rows nor those outside cu[0] .. cu[n_seqs]-1 are written.
+ * max_kv (at most 2^31 - 65) bounds the
+ * keys of any sequence (context and drafts): keys past it are not there
+ * either; 0 means width * page_size.  It may be larger than the lengths are (it
+ * decides how the work is split, not how much there is), so a captured launch
+ * can be replayed as the context grows.
+ *
+ * q  : rows of `dtype`, ldq elements apart, 16-byte aligned, hq heads.
+ * o  : rows of `dtype`, ldo elements apart, or NULL.
+ * oq : Q8_1 blocks [T][hq * head_dim / 32], 4-byte aligned, or NULL: exactly
+ *      skg_quantize_act_q8_1 of the binary32 o.  SKG_F32 only.
+ * ws : skg_tree_attn_workspace(...) bytes, 16-byte aligned, contents not read;
+ *      NULL if that is 0.  Calls that may run at the same time need one each.
+ * Products of a key and a query, probabilities and sums keep binary32's
+ * precision for SKG_F32 (terms of 11 or 8 bits each on the matrix cores) and one
+ * fp16 or bf16 rounding of q and p for SKG_BF16; sums are binary32.  The result
+ * does not change from call to call.  q, o and oq do not overlap.
+ *
+ * T >= 1, n_seqs 1..65535, 1 <= max_draft <= 64, width 1..2^26, scale finite;
+ * hq a multiple of the cache's heads, hq / heads <= 256; T <= 2^24.
+ * Errors: SKG_E_SHAPE (counts, strides, dimensions), SKG_E_INVALID_ARG (null
+ * pointers, both outputs null, scale, unknown types, a short workspace, overlaps), SKG_E_ALIGN,
+ * SKG_E_UNSUPPORTED (oq with SKG_BF16).
+ */
+size_t skg_tree_attn_workspace(const skg_kv_cache* cache, int64_t T, int64_t n_seqs, int hq, int max_draft,
+                               int64_t width, int64_t max_kv);
+skg_status skg_tree_attn(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, int64_t n_seqs, int hq,
+                         int max_draft, const void* q, int64_t ldq, const int32_t* cu, const int32_t* ctx,
+                         const int32_t* table, int64_t width, int64_t max_kv, const uint64_t* mask, float scale,
+                         void* o, int64_t ldo, void* oq, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * Test hook: the int32 block dot products sum_i code_i * qa_i (q4_0) or
  * sum_i q_i * qa_i (q8_0) of rows [n0, n0 + nr) against one Q8_1 activation
  * row, computed by the same device function the gemv kernels use.

@@ -75,3 +75,14 @@ from .gemv import (  # noqa: F401
     tolerance,
     check_close,
 )
+from .attention import (  # noqa: F401
+    KV_FMTS,
+    Pages,
+    kv_decode,
+    kv_encode,
+    rope_ref,
+    rope_tolerance,
+    row_places,
+    tree_attn_ref,
+    tree_attn_tolerance,
+)

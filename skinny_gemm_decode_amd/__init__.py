@@ -82,6 +82,14 @@ def _load() -> ctypes.CDLL:
         "skg_gemv": (i32, [i32, i64, i64, i64, vp, vp, vp, vp]),
         "skg_gemv_multi": (i32, [i32, i64, i64, i32, ctypes.POINTER(i64), vp, vp, ctypes.POINTER(vp), i32, vp]),
         "skg_gemm_tiled": (i32, [i32, i64, i64, i64, vp, vp, vp, vp]),
+        "skg_kv_bytes": (sz, [i32, i32, i32, i32, i64]),
+        "skg_qk_norm_rope": (i32, [i32, i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp]),
+        "skg_kv_store": (i32, [vp, i32, i64, vp, i64, vp, i64, vp, vp]),
+        "skg_kv_load": (i32, [vp, i32, i64, vp, vp, i64, vp, i64, vp]),
+        "skg_qkv_rope_store": (i32, [vp, i32, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
+        "skg_tree_attn_workspace": (sz, [vp, i64, i64, i32, i32, i64, i64]),
+        "skg_tree_attn": (i32, [vp, i32, i64, i64, i32, i32, vp, i64, vp, vp, vp, i64, i64, vp, ctypes.c_float,
+                                vp, i64, vp, vp, sz, vp]),
         "skg_debug_block_dots": (i32, [i32, i64, i64, i64, i64, vp, vp, vp, vp]),
         "skg_stream_read": (i32, [vp, sz, vp, vp]),
         "skg_empty_launch": (i32, [i64, i32, vp]),
@@ -378,3 +386,21 @@ def set_lds_pad(nbytes: int) -> None:
 
 def gemm_tiled_set_variant(variant: int) -> None:
     check(lib.skg_gemm_tiled_set_variant(variant))
+
+
+# ---- rotation, cache and attention ------------------------------------------
+
+from .kv import (  # noqa: E402,F401
+    KV_BF16,
+    KV_Q4_0,
+    KV_Q8_0,
+    KvCache,
+    kv_bytes,
+    kv_cache,
+    kv_load,
+    kv_store,
+    qk_norm_rope,
+    qkv_rope_store,
+    tree_attn,
+    tree_attn_workspace,
+)

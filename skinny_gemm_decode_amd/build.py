@@ -28,7 +28,10 @@ SOURCES = [
     "gemv_q4_0_f32_m68.hip",
     "gemv_q4_0_f32_m35.hip",
     "gemv_q8_0_f32_m38.hip",
+    "rope_kv.hip",
+    "tree_attn.hip",
     "api.hip",
+    "api_kv.hip",
     "pack.hip",
     "quant.hip",
     "norm.hip",

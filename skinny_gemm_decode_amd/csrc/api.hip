@@ -14,16 +14,23 @@
 #include <tuple>
 #include <vector>
 
+#include "api_common.h"
 #include "gemv_registry.h"
 #include "gemv_mfma.h"
 #include "gemv_mfma_pw.h"
 #include "kernels.h"
 
-using namespace skg;
+namespace skg {
 
 namespace {
 
 thread_local char g_err[512] = "";
+
+constexpr int MAX_DEV = 64;
+std::atomic<int> g_dev_state[MAX_DEV];  // 0 unknown, 1 gfx950, 2 other
+std::atomic<int> g_dev_cus[MAX_DEV];
+
+}  // namespace
 
 skg_status fail(skg_status st, const char* fmt, ...) {
   va_list ap;
@@ -38,11 +45,7 @@ skg_status ok() {
   return SKG_OK;
 }
 
-constexpr int MAX_DEV = 64;
-std::atomic<int> g_dev_state[MAX_DEV];  // 0 unknown, 1 gfx950, 2 other
-std::atomic<int> g_dev_cus[MAX_DEV];
-
-skg_status check_device(int* cus = nullptr) {
+skg_status check_device(int* cus) {
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail(SKG_E_DEVICE, "no HIP device (%s)", hipGetErrorString(e));
@@ -61,7 +64,12 @@ skg_status check_device(int* cus = nullptr) {
   return SKG_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace skg
+
+using namespace skg;
+
+namespace {
+
 
 bool is_gemv_fmt(int fmt) {
   return (fmt >= SKG_BF16_BF16 && fmt <= SKG_Q8_0_Q8_1) || (fmt >= SKG_Q4_K_F32 && fmt <= SKG_Q6_K_Q8_1);

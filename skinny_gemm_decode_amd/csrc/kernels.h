@@ -5,6 +5,7 @@
 #include <vector>
 
 #include "common.h"
+#include "kv_layout.h"
 
 namespace skg {
 
@@ -27,5 +28,24 @@ hipError_t launch_gemm_i8(int64_t M, int64_t K, int64_t N, const void* W, const 
                           hipStream_t stream);
 hipError_t launch_gemm_tiled(int64_t M, int64_t K, int64_t N, const void* W, const Layout& L, const void* x,
                              float* y, hipStream_t stream);
+
+// Rotation, cache and attention.  Counts, strides (elements) and pointers are
+// checked by the ABI; hipErrorInvalidValue means more rows than a grid takes.
+hipError_t launch_qk_norm_rope(skg_dtype dt, int64_t T, int hq, int hk, int D, const void* q, int64_t ldq,
+                               const void* k, int64_t ldk, const skg_rope* rope, void* qo, int64_t ldqo, void* ko,
+                               int64_t ldko, hipStream_t stream);
+hipError_t launch_kv_store(const KvView& c, int kind, int D, skg_dtype dt, int64_t T, const void* k, int64_t ldk,
+                           const void* v, int64_t ldv, const int64_t* slots, hipStream_t stream);
+hipError_t launch_kv_load(const KvView& c, int kind, int D, skg_dtype dt, int64_t T, const int64_t* slots, void* k,
+                          int64_t ldk, void* v, int64_t ldv, hipStream_t stream);
+hipError_t launch_qkv_rope_store(const KvView& c, int kind, int D, skg_dtype dt, int64_t T, int hq, const void* q,
+                                 int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                 const skg_rope* rope, const int64_t* slots, void* qo, int64_t ldqo,
+                                 hipStream_t stream);
+struct TreeArgs;
+size_t tree_attn_workspace(int kind, int D, int heads, int64_t T, int64_t n_seqs, int hq, int max_draft,
+                           int64_t max_kv);
+hipError_t launch_tree_attn(const TreeArgs& a, int kind, int D, skg_dtype dt, int heads, void* ws,
+                            hipStream_t stream);
 
 }  // namespace skg

@@ -1,0 +1,545 @@
+// Per-head normalisation and rotation of queries and keys, and the cache's
+// encoder and decoder.
+//
+// Rotation.  Position p turns the pair (a, b) of frequency f_i by th = p f_i:
+//   (a cos th - b sin th, a sin th + b cos th),
+// either adjacent elements or elements half a rotated part apart.  At far
+// positions th is many turns, and its binary32 form would have lost the angle
+// (p = 10^6: 2^-4 of a radian), so th is formed exactly in binary64 (a 24-bit
+// frequency times a 31-bit position), reduced there to within pi/4 and only
+// then evaluated in binary32.  A workgroup computes its token's rot / 2 angles
+// once, one per thread, and its rows read them from LDS.
+//
+// A row is D / 2 units of 16 bytes, two per lane: unit l and the unit half the
+// rotated part further, so both styles of pairing stay within a lane and need
+// no exchange (lanes past the rotated part hold two adjacent units).  The sum
+// of squares meets over the row's 4..32 lanes.
+//
+// Cache rows.  The encoder and decoder give a lane the element pair
+// (2c, 2c + 1) of blocks 2 bp and 2 bp + 1, c = lane & 15: the loads of a
+// 16-lane row are 128 contiguous bytes of binary32, a block's maximum is four
+// DPP steps, and the lane's four codes are adjacent in the cache row.
+#include "kv_common.h"
+#include "kernels.h"
+
+namespace skg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int CTRL>
+__device__ inline int dpp_u(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+
+// Largest value / smallest integer over the 16 lanes of a DPP row, in all of them.
+__device__ inline float row16_max(float v) {
+  v = fmaxf(v, dpp_f<SKG_DPP_QUAD_XOR1>(v));
+  v = fmaxf(v, dpp_f<SKG_DPP_QUAD_XOR2>(v));
+  v = fmaxf(v, dpp_f<SKG_DPP_ROW_HALF_MIRROR>(v));
+  return fmaxf(v, dpp_f<SKG_DPP_ROW_MIRROR>(v));
+}
+__device__ inline int row16_min(int v) {
+  v = min(v, dpp_u<SKG_DPP_QUAD_XOR1>(v));
+  v = min(v, dpp_u<SKG_DPP_QUAD_XOR2>(v));
+  v = min(v, dpp_u<SKG_DPP_ROW_HALF_MIRROR>(v));
+  return min(v, dpp_u<SKG_DPP_ROW_MIRROR>(v));
+}
+// Sum over aligned groups of L lanes (a power of two, 4..32), in all of them.
+template <int L>
+__device__ inline float group_sum(float v) {
+  v += dpp_f<SKG_DPP_QUAD_XOR1>(v);
+  v += dpp_f<SKG_DPP_QUAD_XOR2>(v);
+  if constexpr (L >= 8) v += dpp_f<SKG_DPP_ROW_HALF_MIRROR>(v);
+  if constexpr (L >= 16) v += dpp_f<SKG_DPP_ROW_MIRROR>(v);
+  if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
+// cos and sin of pos * f.  n = nearest multiple of pi/2; what is left of the
+// angle is within pi/4, where the Taylor polynomials below are exact to 2^-28.
+__device__ inline f32x2 cos_sin(int32_t pos, float f) {
+  const double th = double(pos) * double(f);
+  const double n = rint(th * 0.63661977236758134308);
+  const double r64 = fma(-n, 6.123233995736766e-17, fma(-n, 1.5707963267948966, th));
+  const float r = float(r64), z = r * r;
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+  s = fmaf(z, s, 8.3333333e-3f);
+  s = fmaf(z, s, -1.6666667e-1f);
+  s = fmaf(r * z, s, r);
+  float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  c = fmaf(z, c, -1.3888889e-3f);
+  c = fmaf(z, c, 4.1666667e-2f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  // quadrant: n mod 4, from the low bits of the exact integer n
+  const int64_t q = int64_t(n) & 3;
+  const float cq = (q & 1) ? s : c, sq = (q & 1) ? c : s;
+  return f32x2{(q == 1 || q == 2) ? -cq : cq, (q >= 2) ? -sq : sq};
+}
+
+struct RopeArgs {
+  int rot, interleaved, norm;
+  float eps;
+  const int32_t* pos;
+  const float* inv_freq;
+  const float* gq;
+  const float* gk;
+};
+
+// The rows of a tensor: token stride in bytes, heads adjacent.
+struct Rows {
+  uint8_t* p;
+  int64_t ld;
+};
+
+template <class T, int D>
+struct RowShape {
+  static constexpr int kVec = Elem<T>::kVec;
+  static constexpr int kUnits = D / kVec;
+  static constexpr int kLanes = kUnits / 2;          // lanes of a row
+  static constexpr int kRows = kThreads / kLanes;    // rows of a pass
+};
+
+// The two units of lane l: half the rotated part apart within it, adjacent past it.
+template <class T, int D>
+__device__ inline void units_of(int l, int rot, int& ua, int& ub) {
+  const int half = rot / (2 * Elem<T>::kVec);
+  ua = l < half ? l : 2 * l;
+  ub = l < half ? l + half : 2 * l + 1;
+}
+
+// One row in its lanes' registers: normalised (norm) and turned.  Every lane
+// of the row executes it.
+template <class T, int D>
+__device__ inline void norm_rope(float (&a)[Elem<T>::kVec], float (&b)[Elem<T>::kVec], int l, int ua, int ub,
+                                 const RopeArgs& r, const float* g, const f32x2* cs) {
+  constexpr int V = Elem<T>::kVec;
+  if (r.norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+    ss = group_sum<RowShape<T, D>::kLanes>(ss);
+    const float rs = 1.0f / sqrtf(ss / float(D) + r.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      a[i] *= rs;
+      b[i] *= rs;
+    }
+    if (g) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const f32x4 ga = *reinterpret_cast<const f32x4*>(g + ua * V + i);
+        const f32x4 gb = *reinterpret_cast<const f32x4*>(g + ub * V + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[i + j] *= ga[j];
+          b[i + j] *= gb[j];
+        }
+      }
+    }
+  }
+  if (l < r.rot / (2 * V)) {
+    if (r.interleaved) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const f32x2 ca = cs[(ua * V + i) / 2], cb = cs[(ub * V + i) / 2];
+        const float a0 = a[i], b0 = b[i];
+        a[i] = a0 * ca.x - a[i + 1] * ca.y;
+        a[i + 1] = a0 * ca.y + a[i + 1] * ca.x;
+        b[i] = b0 * cb.x - b[i + 1] * cb.y;
+        b[i + 1] = b0 * cb.y + b[i + 1] * cb.x;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const f32x2 c = cs[ua * V + i];
+        const float a0 = a[i];
+        a[i] = a0 * c.x - b[i] * c.y;
+        b[i] = a0 * c.y + b[i] * c.x;
+      }
+    }
+  }
+}
+
+// The angles of token `tok` into cs[0 .. rot / 2).
+__device__ inline void fill_angles(const RopeArgs& r, int64_t tok, f32x2* cs) {
+  const int t = threadIdx.x;
+  if (t < r.rot / 2) cs[t] = cos_sin(r.pos[tok], r.inv_freq[t]);
+}
+
+// P rows per thread, all loaded before the first is used.
+template <class T, int D, int P>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(Rows q, Rows k, Rows qo, Rows ko, int hq, int hk,
+                                                                int chunks, RopeArgs r) {
+  using S = RowShape<T, D>;
+  __shared__ f32x2 cs[D / 2];
+  const int64_t tok = blockIdx.x / unsigned(chunks);
+  const int first = int(blockIdx.x % unsigned(chunks)) * S::kRows * P + threadIdx.x / S::kLanes;
+  const int l = threadIdx.x % S::kLanes;
+  int ua, ub;
+  units_of<T, D>(l, r.rot, ua, ub);
+  u32x4 xa[P], xb[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int row = first + p * S::kRows;
+    if (row < hq + hk) {
+      const bool isq = row < hq;
+      const u32x4* src = reinterpret_cast<const u32x4*>((isq ? q.p : k.p) + tok * (isq ? q.ld : k.ld)) +
+                         (isq ? row : row - hq) * S::kUnits;
+      xa[p] = src[ua];
+      xb[p] = src[ub];
+    }
+  }
+  fill_angles(r, tok, cs);
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int row = first + p * S::kRows;
+    if (row < hq + hk) {
+      const bool isq = row < hq;
+      float a[S::kVec], b[S::kVec];
+      Elem<T>::unpack(xa[p], a);
+      Elem<T>::unpack(xb[p], b);
+      norm_rope<T, D>(a, b, l, ua, ub, r, isq ? r.gq : r.gk, cs);
+      u32x4* dst = reinterpret_cast<u32x4*>((isq ? qo.p : ko.p) + tok * (isq ? qo.ld : ko.ld)) +
+                   (isq ? row : row - hq) * S::kUnits;
+      dst[ua] = Elem<T>::pack(a);
+      dst[ub] = Elem<T>::pack(b);
+    }
+  }
+}
+
+// ---- cache rows -------------------------------------------------------------
+
+template <int D>
+struct PairShape {
+  static constexpr int kLanes = D / 4;              // lanes of a row
+  static constexpr int kRows = kThreads / kLanes;   // rows of a pass
+};
+
+__device__ inline int round_code(float x, float id, int lo, int hi) {
+#pragma clang fp contract(off)
+  return int(fminf(fmaxf(roundf(x * id), float(lo)), float(hi)));
+}
+__device__ inline uint32_t scale16(float d) {
+  return __half_as_ushort(__float2half_rn(fminf(fmaxf(d, -65504.f), 65504.f)));
+}
+
+// One block's pair (x, y) = elements 2c, 2c + 1 from each of 16 lanes: the
+// codes (x low) and the scale.  q8_0 codes are offset by 128, q4_0's by 8.
+template <int KIND>
+__device__ inline void encode_pair(float x, float y, int c, uint32_t& qx, uint32_t& qy, uint32_t& s) {
+#pragma clang fp contract(off)
+  const float ax = fabsf(x), ay = fabsf(y), amax = row16_max(fmaxf(ax, ay));
+  if constexpr (KIND == KV_Q8_0) {
+    const float d = amax / 127.0f, id = q8_1_id(d);
+    qx = uint32_t(round_code(x, id, -127, 127) + 128);
+    qy = uint32_t(round_code(y, id, -127, 127) + 128);
+    s = scale16(d);
+  } else {
+    // the first element of magnitude amax: its index and, in bit 0, its sign
+    const int ix = ax == amax ? 4 * c + int(__float_as_uint(x) >> 31) : 4096;
+    const int iy = ay == amax ? 4 * c + 2 + int(__float_as_uint(y) >> 31) : 4096;
+    const int at = row16_min(min(ix, iy));
+    const float m = (at & 1) ? -amax : amax;
+    const float d = m / -8.0f, id = q8_1_id(d);
+    qx = uint32_t(round_code(x, id, -8, 7) + 8);
+    qy = uint32_t(round_code(y, id, -8, 7) + 8);
+    s = scale16(d);
+  }
+}
+
+// A cache row from its D / 4 lanes: lane (c, bp) holds x = elements 2c, 2c + 1
+// of block 2 bp and y those of block 2 bp + 1.  chunk: the (page, head)'s.
+template <int KIND, int D>
+__device__ inline void put_row(uint8_t* chunk, uint32_t shift, uint32_t tok, int c, int bp, f32x2 x, f32x2 y,
+                               bool store) {
+  uint8_t* row = chunk + kv_codes_at(KIND, D, tok);
+  if constexpr (KIND == KV_BF16) {
+    if (store) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(row) + 32 * bp + c;
+      w[0] = bf16_pair(x.x, x.y);
+      w[16] = bf16_pair(y.x, y.y);
+    }
+  } else {
+    constexpr int NB = D / 32;
+    uint32_t a0, a1, b0, b1, s0, s1;
+    encode_pair<KIND>(x.x, x.y, c, a0, a1, s0);
+    encode_pair<KIND>(y.x, y.y, c, b0, b1, s1);
+    if (store) {
+      if constexpr (KIND == KV_Q8_0)
+        *reinterpret_cast<uint32_t*>(row + 2 * NB * c + 4 * bp) = a0 | (a1 << 8) | (b0 << 16) | (b1 << 24);
+      else
+        *reinterpret_cast<uint16_t*>(row + NB * c + 2 * bp) = uint16_t(a0 | (a1 << 4) | (b0 << 8) | (b1 << 12));
+      if (c == 0)
+        *reinterpret_cast<uint32_t*>(chunk + kv_scales_at(KIND, D, shift, tok) + 4 * bp) = s0 | (s1 << 16);
+    }
+  }
+}
+
+template <int KIND, int D>
+__device__ inline void get_row(const uint8_t* chunk, uint32_t shift, uint32_t tok, int c, int bp, f32x2& x,
+                               f32x2& y) {
+  const uint8_t* row = chunk + kv_codes_at(KIND, D, tok);
+  if constexpr (KIND == KV_BF16) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + 32 * bp + c;
+    x = f32x2{bf16_lo(w[0]), bf16_hi(w[0])};
+    y = f32x2{bf16_lo(w[16]), bf16_hi(w[16])};
+  } else {
+    constexpr int NB = D / 32;
+    const uint32_t s = *reinterpret_cast<const uint32_t*>(chunk + kv_scales_at(KIND, D, shift, tok) + 4 * bp);
+    const float d0 = h2f(s & 0xFFFFu), d1 = h2f(s >> 16);
+    if constexpr (KIND == KV_Q8_0) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 2 * NB * c + 4 * bp);
+      x = f32x2{d0 * (cvt_ubyte<0>(w) - 128.f), d0 * (cvt_ubyte<1>(w) - 128.f)};
+      y = f32x2{d1 * (cvt_ubyte<2>(w) - 128.f), d1 * (cvt_ubyte<3>(w) - 128.f)};
+    } else {
+      const uint32_t w = *reinterpret_cast<const uint16_t*>(row + NB * c + 2 * bp);
+      x = f32x2{d0 * (float(w & 15u) - 8.f), d0 * (float((w >> 4) & 15u) - 8.f)};
+      y = f32x2{d1 * (float((w >> 8) & 15u) - 8.f), d1 * (float(w >> 12) - 8.f)};
+    }
+  }
+}
+
+// Keys (blockIdx.y == 0) or values of P rows per thread into the cache.
+template <class T, int KIND, int D, int P>
+__global__ __launch_bounds__(kThreads) void kv_store_kernel(KvView cache, Rows k, Rows v, const int64_t* slots,
+                                                            int64_t rows) {
+  constexpr int L = PairShape<D>::kLanes;
+  const Rows in = blockIdx.y ? v : k;
+  uint8_t* buf = blockIdx.y ? cache.v : cache.k;
+  const int lane = threadIdx.x % L, c = lane & 15, bp = lane >> 4;
+  const int64_t first = int64_t(blockIdx.x) * PairShape<D>::kRows * P + threadIdx.x / L;
+  f32x2 x[P], y[P];
+  int64_t slot[P];
+  uint32_t head[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int64_t r = first + p * PairShape<D>::kRows;
+    slot[p] = -1;
+    x[p] = y[p] = f32x2{0.f, 0.f};
+    head[p] = 0;
+    if (r < rows) {
+      const uint32_t tok = uint32_t(r / cache.heads);
+      head[p] = uint32_t(r - int64_t(tok) * cache.heads);
+      const uint8_t* src = in.p + tok * in.ld + (int64_t(head[p]) * D + 64 * bp + 2 * c) * int(sizeof(T));
+      x[p] = Elem<T>::pair(src);
+      y[p] = Elem<T>::pair(src + 32 * sizeof(T));
+      slot[p] = slots[tok];
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const bool in_cache = kv_slot_in(cache, slot[p]);
+    const int64_t s = in_cache ? slot[p] : 0;
+    put_row<KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head[p]), cache.shift,
+                     uint32_t(s & ((int64_t(1) << cache.shift) - 1)), c, bp, x[p], y[p], in_cache);
+  }
+}
+
+template <class T, int KIND, int D, int P>
+__global__ __launch_bounds__(kThreads) void kv_load_kernel(KvView cache, Rows k, Rows v, const int64_t* slots,
+                                                           int64_t rows) {
+  constexpr int L = PairShape<D>::kLanes;
+  const Rows out = blockIdx.y ? v : k;
+  const uint8_t* buf = blockIdx.y ? cache.v : cache.k;
+  const int lane = threadIdx.x % L, c = lane & 15, bp = lane >> 4;
+  const int64_t first = int64_t(blockIdx.x) * PairShape<D>::kRows * P + threadIdx.x / L;
+  f32x2 x[P], y[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int64_t r = first + p * PairShape<D>::kRows;
+    x[p] = y[p] = f32x2{0.f, 0.f};
+    if (r < rows) {
+      const uint32_t tok = uint32_t(r / cache.heads), head = uint32_t(r - int64_t(tok) * cache.heads);
+      const int64_t s = slots[tok];
+      if (kv_slot_in(cache, s))
+        get_row<KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
+                         uint32_t(s & ((int64_t(1) << cache.shift) - 1)), c, bp, x[p], y[p]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int64_t r = first + p * PairShape<D>::kRows;
+    if (r < rows) {
+      const uint32_t tok = uint32_t(r / cache.heads), head = uint32_t(r - int64_t(tok) * cache.heads);
+      uint8_t* dst = out.p + tok * out.ld + (int64_t(head) * D + 64 * bp + 2 * c) * int(sizeof(T));
+      Elem<T>::put_pair(dst, x[p].x, x[p].y);
+      Elem<T>::put_pair(dst + 32 * sizeof(T), y[p].x, y[p].y);
+    }
+  }
+}
+
+// Rotation and store in one launch.  Workgroups 0 .. rope_chunks - 1 of a
+// token take its query and key rows; a key row passes through LDS (binary32)
+// from the rotation's lanes to the encoder's.  The others take value rows.
+template <class T, int KIND, int D>
+__global__ __launch_bounds__(kThreads) void qkv_rope_store_kernel(KvView cache, Rows q, Rows k, Rows v, Rows qo,
+                                                                  int hq, int rope_chunks, int chunks,
+                                                                  const int64_t* slots, RopeArgs r) {
+  using S = RowShape<T, D>;
+  using E = PairShape<D>;
+  __shared__ f32x2 cs[D / 2];
+  __shared__ __attribute__((aligned(16))) float rows_f32[S::kRows * D];
+  const int64_t tok = blockIdx.x / unsigned(chunks);
+  const int chunk = int(blockIdx.x % unsigned(chunks));
+  const int hk = int(cache.heads);
+  const int64_t slot = slots[tok];
+  const bool in_cache = kv_slot_in(cache, slot);
+  const int64_t s = in_cache ? slot : 0;
+  const int64_t page = s >> cache.shift;
+  const uint32_t at = uint32_t(s & ((int64_t(1) << cache.shift) - 1));
+  const int lane = threadIdx.x % E::kLanes, c = lane & 15, bp = lane >> 4;
+  if (chunk >= rope_chunks) {  // uniform over the workgroup
+    const int head = (chunk - rope_chunks) * E::kRows + threadIdx.x / E::kLanes;
+    f32x2 x{0.f, 0.f}, y{0.f, 0.f};
+    if (head < hk) {
+      const uint8_t* src = v.p + tok * v.ld + (int64_t(head) * D + 64 * bp + 2 * c) * int(sizeof(T));
+      x = Elem<T>::pair(src);
+      y = Elem<T>::pair(src + 32 * sizeof(T));
+    }
+    put_row<KIND, D>(cache.v + kv_chunk_at(cache, page, head < hk ? head : 0), cache.shift, at, c, bp, x, y,
+                     in_cache && head < hk);
+    return;
+  }
+  const int first = chunk * S::kRows, row = first + threadIdx.x / S::kLanes, l = threadIdx.x % S::kLanes;
+  const bool isq = row < hq, is = row < hq + hk;
+  int ua, ub;
+  units_of<T, D>(l, r.rot, ua, ub);
+  u32x4 xa{}, xb{};
+  if (is) {
+    const u32x4* src = reinterpret_cast<const u32x4*>((isq ? q.p : k.p) + tok * (isq ? q.ld : k.ld)) +
+                       (isq ? row : row - hq) * S::kUnits;
+    xa = src[ua];
+    xb = src[ub];
+  }
+  fill_angles(r, tok, cs);
+  __syncthreads();
+  float a[S::kVec], b[S::kVec];
+  Elem<T>::unpack(xa, a);
+  Elem<T>::unpack(xb, b);
+  if (is) norm_rope<T, D>(a, b, l, ua, ub, r, isq ? r.gq : r.gk, cs);
+  if (isq) {
+    u32x4* dst = reinterpret_cast<u32x4*>(qo.p + tok * qo.ld) + row * S::kUnits;
+    dst[ua] = Elem<T>::pack(a);
+    dst[ub] = Elem<T>::pack(b);
+  } else if (is) {
+    float* dst = rows_f32 + (row - first) * D;
+#pragma unroll
+    for (int i = 0; i < S::kVec; i += 4) {
+      *reinterpret_cast<f32x4*>(dst + ua * S::kVec + i) = f32x4{a[i], a[i + 1], a[i + 2], a[i + 3]};
+      *reinterpret_cast<f32x4*>(dst + ub * S::kVec + i) = f32x4{b[i], b[i + 1], b[i + 2], b[i + 3]};
+    }
+  }
+  if (first + S::kRows <= hq) return;  // no key row here (uniform)
+  __syncthreads();
+  for (int i = threadIdx.x / E::kLanes; i < S::kRows; i += E::kRows) {
+    const int head = first + i - hq;
+    const bool here = head >= 0 && head < hk;
+    f32x2 x{0.f, 0.f}, y{0.f, 0.f};
+    if (here) {
+      x = *reinterpret_cast<const f32x2*>(rows_f32 + i * D + 64 * bp + 2 * c);
+      y = *reinterpret_cast<const f32x2*>(rows_f32 + i * D + 64 * bp + 32 + 2 * c);
+    }
+    put_row<KIND, D>(cache.k + kv_chunk_at(cache, page, here ? head : 0), cache.shift, at, c, bp, x, y,
+                     in_cache && here);
+  }
+}
+
+RopeArgs rope_args(const skg_rope* r) {
+  return RopeArgs{r->rot, r->interleaved, r->norm, r->eps, r->pos, r->inv_freq, r->gq, r->gk};
+}
+
+Rows rows_of(const void* p, int64_t ld, skg_dtype dt) {
+  return Rows{static_cast<uint8_t*>(const_cast<void*>(p)), ld * (dt == SKG_F32 ? 4 : 2)};
+}
+
+// Calls f with the type, cache kind and head size as template arguments.
+template <class F>
+hipError_t by_type(skg_dtype dt, F&& f) {
+  return dt == SKG_F32 ? f(float{}) : f(__bf16{});
+}
+template <class F>
+hipError_t by_dim(int D, F&& f) {
+  return D == 64 ? f(std::integral_constant<int, 64>{})
+                 : D == 128 ? f(std::integral_constant<int, 128>{}) : f(std::integral_constant<int, 256>{});
+}
+template <class F>
+hipError_t by_kind(int kind, F&& f) {
+  return kind == KV_BF16 ? f(std::integral_constant<int, KV_BF16>{})
+                         : kind == KV_Q8_0 ? f(std::integral_constant<int, KV_Q8_0>{})
+                                           : f(std::integral_constant<int, KV_Q4_0>{});
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(skg_dtype dt, int64_t T, int hq, int hk, int D, const void* q, int64_t ldq,
+                               const void* k, int64_t ldk, const skg_rope* rope, void* qo, int64_t ldqo, void* ko,
+                               int64_t ldko, hipStream_t stream) {
+  return by_type(dt, [&](auto t) {
+    return by_dim(D, [&](auto d) {
+      using E = decltype(t);
+      constexpr int N = RowShape<E, d()>::kRows;
+      const int64_t chunks = (hq + hk + N - 1) / N;
+      if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
+      hipLaunchKernelGGL((qk_norm_rope_kernel<E, d(), 1>), dim3(unsigned(T * chunks)), dim3(kThreads), 0, stream,
+                         rows_of(q, ldq, dt), rows_of(k, ldk, dt), rows_of(qo, ldqo, dt), rows_of(ko, ldko, dt), hq,
+                         hk, int(chunks), rope_args(rope));
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_kv_store(const KvView& c, int kind, int D, skg_dtype dt, int64_t T, const void* k, int64_t ldk,
+                           const void* v, int64_t ldv, const int64_t* slots, hipStream_t stream) {
+  return by_type(dt, [&](auto t) {
+    return by_dim(D, [&](auto d) {
+      return by_kind(kind, [&](auto kd) {
+        const int64_t rows = T * c.heads, grid = (rows + PairShape<d()>::kRows - 1) / PairShape<d()>::kRows;
+        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((kv_store_kernel<decltype(t), kd(), d(), 1>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
+                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, rows);
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+hipError_t launch_kv_load(const KvView& c, int kind, int D, skg_dtype dt, int64_t T, const int64_t* slots, void* k,
+                          int64_t ldk, void* v, int64_t ldv, hipStream_t stream) {
+  return by_type(dt, [&](auto t) {
+    return by_dim(D, [&](auto d) {
+      return by_kind(kind, [&](auto kd) {
+        const int64_t rows = T * c.heads, grid = (rows + PairShape<d()>::kRows - 1) / PairShape<d()>::kRows;
+        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((kv_load_kernel<decltype(t), kd(), d(), 1>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
+                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, rows);
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+hipError_t launch_qkv_rope_store(const KvView& c, int kind, int D, skg_dtype dt, int64_t T, int hq, const void* q,
+                                 int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                 const skg_rope* rope, const int64_t* slots, void* qo, int64_t ldqo,
+                                 hipStream_t stream) {
+  return by_type(dt, [&](auto t) {
+    return by_dim(D, [&](auto d) {
+      return by_kind(kind, [&](auto kd) {
+        using E = decltype(t);
+        constexpr int N = RowShape<E, d()>::kRows, M = PairShape<d()>::kRows;
+        const int64_t rope_chunks = (hq + int(c.heads) + N - 1) / N, chunks = rope_chunks + (c.heads + M - 1) / M;
+        if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((qkv_rope_store_kernel<E, kd(), d()>), dim3(unsigned(T * chunks)), dim3(kThreads), 0,
+                           stream, c, rows_of(q, ldq, dt), rows_of(k, ldk, dt), rows_of(v, ldv, dt),
+                           rows_of(qo, ldqo, dt), hq, int(rope_chunks), int(chunks), slots, rope_args(rope));
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+}  // namespace skg
