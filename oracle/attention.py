@@ -150,7 +150,7 @@ def tree_attn_ref(q, k, v, sees, scale):
     return o, a, e
 
 
-def tree_attn_tolerance(o, a, e, D, bf16_rows, bf16_cache):
+def tree_attn_tolerance(o, a, e, D, bf16_rows, bf16_cache, keys=0, vmax=0.0):
     """Bound on |o_gpu - o|.
 
     A score's error d makes p wrong by a factor e^(2 d) at most against the
@@ -159,9 +159,15 @@ def tree_attn_tolerance(o, a, e, D, bf16_rows, bf16_cache):
     D products (D u each, u = 2^-24, + 8 u for scales and exp's argument); p
     to 2^-17, sums over keys in tiles 2^-17.  bf16 rows: q and p are rounded
     once, to fp16 (half a step 2^-11) or for a bf16 cache to bf16 (2^-8), and
-    o once to bf16 (2^-8)."""
+    o once to bf16 (2^-8).
+
+    p times a key's scale is held in fp16, whose smallest step is 2^-24, with
+    the largest scale (up to three bits below its bound) and p = 1 at 2^11: a
+    term is off by half a step, 2^-25 / 2^(11 - 3) = 2^-33 of the largest value
+    vmax, each of `keys` keys once (quantised caches)."""
     u = 2.0**-24
+    floor = 0.0 if bf16_cache else keys * 2.0**-33 * vmax
     if not bf16_rows:
-        return a * (2 * e * (2.0**-21 + (D + 8) * u) + 2.0**-16) + 1e-30
+        return a * (2 * e * (2.0**-21 + (D + 8) * u) + 2.0**-16) + floor + 1e-30
     r = 2.0**-8 if bf16_cache else 2.0**-11
-    return a * (np.expm1(2 * e * (r + (D + 8) * u)) + 2 * r + 2.0**-16) + 2.0**-8 * np.abs(o) + 1e-30
+    return a * (np.expm1(2 * e * (r + (D + 8) * u)) + 2 * r + 2.0**-16) + 2.0**-8 * np.abs(o) + floor + 1e-30

@@ -30,6 +30,12 @@ SOURCES = [
     "gemv_q8_0_f32_m38.hip",
     "rope_kv.hip",
     "tree_attn.hip",
+    "tree_attn_bf16_f32.hip",
+    "tree_attn_bf16_bf16.hip",
+    "tree_attn_q8_0_f32.hip",
+    "tree_attn_q8_0_bf16.hip",
+    "tree_attn_q4_0_f32.hip",
+    "tree_attn_q4_0_bf16.hip",
     "api.hip",
     "api_kv.hip",
     "pack.hip",

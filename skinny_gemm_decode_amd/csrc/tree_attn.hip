@@ -1,105 +1,143 @@
-// Attention of drafted tokens over a paged cache.
-//
-// One wave per (token, query head) walks the keys once with the running
-// maximum m and sum l of the softmax: for a new score s,
-//   m' = max(m, s),  l = l e^(m - m') + e^(s - m'),  o = o e^(m - m') + e^(s - m') v.
-// Each lane holds D / 64 elements of the row.
+// How an attention call is split, and the join of its splits' partial results.
 #include "tree_attn.h"
-#include "kernels.h"
+#include "tree_attn_instances.h"
 
 namespace skg {
 
 namespace {
 
-// Element e of token t of a chunk.
-template <int KIND, int D>
-__device__ inline float cache_value(const uint8_t* chunk, uint32_t shift, uint32_t t, int e) {
-  const uint8_t* row = chunk + kv_codes_at(KIND, D, t);
-  if constexpr (KIND == KV_BF16) return bf16_lo(reinterpret_cast<const uint16_t*>(row)[e]);
-  constexpr int NB = D / 32;
-  const int b = e / 32, c = (e % 32) / 2, i = e & 1;
-  const float d = h2f(reinterpret_cast<const uint16_t*>(chunk + kv_scales_at(KIND, D, shift, t))[b]);
-  if constexpr (KIND == KV_Q8_0) return d * (float(row[2 * NB * c + 2 * b + i]) - 128.f);
-  return d * (float((row[NB * c + b] >> (4 * i)) & 15) - 8.f);
+// Joins the splits of a row: with M* the largest M, o = sum 2^(M - M*) o_s and
+// l likewise.  A row's D / 8 threads of 8 elements are repeated over `par`
+// lanes of splits, which meet in LDS.
+template <class T, int D>
+__global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeArgs a, float unit, int par) {
+  constexpr int EPT = 8, kRow = D / EPT;   // threads of a row
+  constexpr int kSlots = 256 / kRow;       // rows times split lanes of a workgroup
+  __shared__ __attribute__((aligned(16))) float buf[kSlots][D];
+  __shared__ float ml[kSlots][2];
+  const int slot = threadIdx.x / kRow, e = (threadIdx.x % kRow) * EPT;
+  const int lane = slot % par, nrow = kSlots / par;
+  // rows (i, head) of sequence blockIdx.y
+  const KvSpan sp = span_of(a, blockIdx.y);
+  const int r = int(blockIdx.x) * nrow + slot / par;
+  const bool is = r < sp.n * a.hq;
+  if (int(blockIdx.x) * nrow >= sp.n * a.hq) return;  // uniform
+  const int64_t tok = sp.t0 + (is ? r / a.hq : 0);
+  const int hd = is ? r % a.hq : 0;
+  const int per = steps_per_split(sp.keys, a.splits);
+  const int steps = sp.keys / kStep + (sp.keys % kStep != 0);
+  int n = (steps + per - 1) / per;
+  n = n < 1 ? 1 : n;
+  const int64_t at = (tok * a.hq + hd) * a.splits;
+  const float* po = a.ws + at * D + e;
+  const float* pm = a.ws + a.T * a.hq * int64_t(a.splits) * D + 2 * at;
+  float M = kNoMax, l = 0.f, y[EPT];
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) y[j] = 0.f;
+  if (is)
+    for (int s = lane; s < n; s += par) {
+      const float ms = pm[2 * s], ls = pm[2 * s + 1];
+      const f32x4 o0 = *reinterpret_cast<const f32x4*>(po + int64_t(s) * D);
+      const f32x4 o1 = *reinterpret_cast<const f32x4*>(po + int64_t(s) * D + 4);
+      const float m = fmaxf(M, ms), f = exp2_fast(M - m), g = exp2_fast(ms - m);
+      M = m;
+      l = fmaf(l, f, ls * g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = fmaf(y[j], f, o0[j] * g);
+        y[4 + j] = fmaf(y[4 + j], f, o1[j] * g);
+      }
+    }
+  if (par > 1) {  // uniform
+#pragma unroll
+    for (int j = 0; j < EPT; j += 4) *reinterpret_cast<f32x4*>(&buf[slot][e + j]) = f32x4{y[j], y[j + 1], y[j + 2], y[j + 3]};
+    if (e == 0) {
+      ml[slot][0] = M;
+      ml[slot][1] = l;
+    }
+    __syncthreads();
+    const int first = slot - lane;
+    M = kNoMax;
+    for (int s = 0; s < par; ++s) M = fmaxf(M, ml[first + s][0]);
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) y[j] = 0.f;
+    for (int s = 0; s < par; ++s) {
+      const float f = exp2_fast(ml[first + s][0] - M);
+      l = fmaf(ml[first + s][1], f, l);
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) y[j] = fmaf(buf[first + s][e + j], f, y[j]);
+    }
+  }
+  const float inv = unit / l;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
+  put_out<T, EPT>(a, tok, int64_t(hd) * D + e, y, is && lane == 0);
 }
 
-template <class T, int KIND, int D>
-__global__ __launch_bounds__(64) void tree_attn_kernel(TreeArgs a) {
-  constexpr int E = D / 64;
-  const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z, lane = threadIdx.x;
-  const int64_t per = a.T / a.n_seqs;
-  const int64_t t0 = a.cu ? a.cu[b] : b * per, t1 = a.cu ? a.cu[b + 1] : (b + 1) * per;
-  const KvSpan sp = kv_span(a.ctx[b], int32_t(t0), int32_t(t1), a.T, a.max_draft, a.max_kv);
-  if (i >= sp.n) return;
-  const int64_t tok = sp.t0 + i;
-  const uint64_t mask = a.mask ? a.mask[tok] : ~uint64_t(0) >> (63 - i);
-  const T* q = reinterpret_cast<const T*>(a.q + tok * a.ldq) + h * D;
-  float x[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = float(q[lane * E + e]) * a.scale;
-    o[e] = 0.f;
-  }
-  const uint32_t head = h / a.group, in_page = (1u << a.cache.shift) - 1;
-  for (int j = 0; j < sp.keys; ++j) {
-    if (j >= sp.ctx && !((mask >> (j - sp.ctx)) & 1)) continue;
-    const int32_t page = a.table[b * a.width + (j >> a.cache.shift)];
-    if (!kv_page_in(a.cache, page)) continue;
-    const uint64_t at = kv_chunk_at(a.cache, page, head);
-    const uint32_t t = uint32_t(j) & in_page;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], cache_value<KIND, D>(a.cache.k + at, a.cache.shift, t, lane * E + e), s);
-    s = wave_sum(s);
-    const float mn = fmaxf(m, s), f = expf(m - mn), p = expf(s - mn);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * f + p * cache_value<KIND, D>(a.cache.v + at, a.cache.shift, t, lane * E + e);
-  }
-  __shared__ float out[D];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    o[e] = l == 0.f ? 0.f : o[e] / l;
-    out[lane * E + e] = o[e];
-    if (a.o) reinterpret_cast<T*>(a.o + tok * a.ldo)[h * D + lane * E + e] = T(o[e]);
-  }
-  __syncthreads();
-  if (a.oq && lane < D / 32) {
-    float v[QK];
-#pragma unroll
-    for (int e = 0; e < QK; ++e) v[e] = out[lane * QK + e];
-    const Q8_1Block blk = quantize_block_q8_1(v);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.oq + ((tok * a.hq + h) * (D / QK) + lane) * 36);
-    dst[0] = blk.d16 | (blk.s16 << 16);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dst[1 + k] = blk.q[k];
-  }
-}
-
-template <class T, int KIND, int D>
-hipError_t go(const TreeArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((tree_attn_kernel<T, KIND, D>), dim3(unsigned(a.hq), unsigned(a.max_draft), unsigned(a.n_seqs)),
-                     dim3(64), 0, stream, a);
+template <class T, int D>
+hipError_t join(const TreeArgs& a, float unit, hipStream_t stream) {
+  constexpr int kSlots = 256 / (D / 8);
+  int par = 1;
+  while (par < a.splits && par < kSlots) par *= 2;
+  const int nrow = kSlots / par;
+  const int64_t rows = int64_t(a.max_draft) * a.hq;
+  hipLaunchKernelGGL((tree_attn_join_kernel<T, D>), dim3(unsigned((rows + nrow - 1) / nrow), unsigned(a.n_seqs)),
+                     dim3(256), 0, stream, a, unit, par);
   return hipGetLastError();
 }
-template <class T, int KIND>
-hipError_t by_dim(int D, const TreeArgs& a, hipStream_t s) {
-  return D == 64 ? go<T, KIND, 64>(a, s) : D == 128 ? go<T, KIND, 128>(a, s) : go<T, KIND, 256>(a, s);
-}
 template <class T>
-hipError_t by_kind(int kind, int D, const TreeArgs& a, hipStream_t s) {
-  return kind == KV_BF16 ? by_dim<T, KV_BF16>(D, a, s)
-                         : kind == KV_Q8_0 ? by_dim<T, KV_Q8_0>(D, a, s) : by_dim<T, KV_Q4_0>(D, a, s);
+hipError_t join_dim(const TreeArgs& a, int D, float unit, hipStream_t s) {
+  return D == 64 ? join<T, 64>(a, unit, s) : D == 128 ? join<T, 128>(a, unit, s) : join<T, 256>(a, unit, s);
+}
+
+struct Plan {
+  int rt, row_groups, splits;
+};
+
+// Two row tiles of 16 a wave where there are more rows than one tile has: the
+// keys' conversion then serves both.  The keys are split until there are two
+// workgroups for each of 256 CUs, but none into less than two steps a wave.
+Plan plan(int heads, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
+  Plan p;
+  const int64_t rows = int64_t(max_draft) * (hq / heads);
+  p.rt = rows <= 16 ? 1 : 2;
+  p.row_groups = int((rows + 16 * p.rt - 1) / (16 * p.rt));
+  const int64_t units = n_seqs * heads * p.row_groups, steps = (max_kv + kStep - 1) / kStep;
+  int64_t s = (512 + units - 1) / units;
+  const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
+  s = s < most ? s : most;
+  p.splits = int(s < 1 ? 1 : s);
+  return p;
 }
 
 }  // namespace
 
-size_t tree_attn_workspace(int, int, int, int64_t, int64_t, int, int, int64_t) { return 0; }
+size_t tree_attn_workspace(int, int D, int heads, int64_t T, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
+  const Plan p = plan(heads, n_seqs, hq, max_draft, max_kv);
+  return p.splits == 1 ? 0 : size_t(T) * size_t(hq) * size_t(p.splits) * size_t(D + 2) * sizeof(float);
+}
 
-hipError_t launch_tree_attn(const TreeArgs& a, int kind, int D, skg_dtype dt, int, void*, hipStream_t stream) {
-  return dt == SKG_F32 ? by_kind<float>(kind, D, a, stream) : by_kind<__bf16>(kind, D, a, stream);
+hipError_t launch_tree_attn(const TreeArgs& args, int kind, int D, skg_dtype dt, int heads, void* ws,
+                            hipStream_t stream) {
+  TreeArgs a = args;
+  const Plan p = plan(heads, a.n_seqs, a.hq, a.max_draft, a.max_kv);
+  a.splits = p.splits;
+  a.row_groups = p.row_groups;
+  a.ws = static_cast<float*>(ws);
+  a.blocks = int64_t(a.hq) * D / QK;
+  const int64_t grid = int64_t(heads) * p.splits * p.row_groups * a.n_seqs;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const bool f32 = dt == SKG_F32;
+  hipError_t e;
+  switch (kind) {
+    case KV_BF16: e = f32 ? tree_attn_bf16_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_bf16_bf16(a, D, p.rt, unsigned(grid), stream); break;
+    case KV_Q8_0: e = f32 ? tree_attn_q8_0_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_q8_0_bf16(a, D, p.rt, unsigned(grid), stream); break;
+    default: e = f32 ? tree_attn_q4_0_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_q4_0_bf16(a, D, p.rt, unsigned(grid), stream); break;
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  const float unit = kind == KV_BF16 ? 1.f : kCodeScale;
+  return f32 ? join_dim<float>(a, D, unit, stream) : join_dim<__bf16>(a, D, unit, stream);
 }
 
 }  // namespace skg

@@ -98,8 +98,10 @@ class Problem:
                     slots[j // self.page == dp] = 0
             r = slice(self.cu[b], self.cu[b] + t)
             scale = 1 / np.sqrt(self.D)
-            o[r], a, e = oracle.tree_attn_ref(self.q[r], self.kp.get(slots), self.vp.get(slots), s, scale)
-            tol[r] = oracle.tree_attn_tolerance(o[r], a, e, self.D, self.bf16, self.fmt == "bf16")
+            v = self.vp.get(slots)
+            o[r], a, e = oracle.tree_attn_ref(self.q[r], self.kp.get(slots), v, s, scale)
+            vmax = np.max(np.abs(v), where=np.isfinite(v), initial=0.0)
+            tol[r] = oracle.tree_attn_tolerance(o[r], a, e, self.D, self.bf16, self.fmt == "bf16", len(slots), vmax)
             done[r] = True
         return o, tol, done
 
