@@ -413,7 +413,9 @@ skg_status skg_qkv_rope_store(const skg_kv_cache* cache, skg_dtype dtype, int64_
  * context and the drafted tokens j of its sequence with bit j of its mask set
  * (mask: uint64 [T]; NULL is a chain, j <= i).
  *   s_j = scale * <q, k_j>,  o = sum_j e^(s_j - max s) v_j / sum_j e^(s_j - max s)
- * over the keys that it sees; a token that sees none gets 0.  Keys on a page
+ * over the keys that it sees; a token that sees none gets 0, and a bf16 value
+ * that is infinite or NaN makes that element NaN where it is seen (only there).
+ * Keys on a page
  * outside the cache or past the table's width are not there.  Query head h
  * reads cache head h / (hq / heads).
  *

@@ -117,9 +117,32 @@ __device__ inline void split_pair(float a, float b, uint32_t (&t)[NT]) {
   }
 }
 
-// Two unsigned bytes in 16-bit halves are fp16 subnormals n 2^-24; one packed
-// fma makes them (n - zero) 2^-9, exactly.  mul = 2^15 (2^11 for a high nibble,
-// which arrives as 16 n).
+// The terms of (p0 s0, p1 s1), s the low or high fp16 of w0 and w1: the rounded
+// products, and with NT = 2 what each leaves.  Written as fused operations
+// whose operands are widened fp16 values, which the compiler turns into one
+// mixed-precision instruction a term; a plain product is formed in binary32
+// and converted (2.5 times the instructions).
+template <int NT>
+__device__ inline void scaled_pair(float p0, float p1, uint32_t w0, uint32_t w1, int high, uint32_t (&t)[NT]) {
+  const f16x2 a = __builtin_bit_cast(f16x2, w0), b = __builtin_bit_cast(f16x2, w1);
+  const _Float16 s0 = high ? a.y : a.x, s1 = high ? b.y : b.x;
+  const _Float16 h0 = static_cast<_Float16>(__builtin_fmaf(p0, float(s0), 0.f));
+  const _Float16 h1 = static_cast<_Float16>(__builtin_fmaf(p1, float(s1), 0.f));
+  t[0] = __builtin_bit_cast(uint32_t, f16x2{h0, h1});
+  if constexpr (NT > 1) {
+    const _Float16 l0 = static_cast<_Float16>(__builtin_fmaf(p0, float(s0), -float(h0)));
+    const _Float16 l1 = static_cast<_Float16>(__builtin_fmaf(p1, float(s1), -float(h1)));
+    t[1] = __builtin_bit_cast(uint32_t, f16x2{l0, l1});
+  }
+}
+
+// Codes as fp16.  Two unsigned bytes in 16-bit halves are the fp16 subnormals
+// n 2^-24, which the matrix instructions take as they are: K's operand is that
+// (a high nibble is 16 n, against q / 16), and the zero of the codes is taken
+// off by the product's initial value, -zero 2^-24 sum q of the block, which is
+// constant for a row.  For V the same would leave differences of long sums, so
+// one packed fma makes (n - zero) 2^-9 of them, exactly (mul = 2^15, or 2^11
+// for a high nibble).
 __device__ inline uint32_t f16_codes(uint32_t x, float mul, float zero) {
   const f16x2 m = {static_cast<_Float16>(mul), static_cast<_Float16>(mul)};
   const f16x2 z = {static_cast<_Float16>(-zero), static_cast<_Float16>(-zero)};
@@ -128,7 +151,10 @@ __device__ inline uint32_t f16_codes(uint32_t x, float mul, float zero) {
 __device__ inline uint32_t q8_pair(uint32_t x) { return f16_codes(x, 32768.f, 0.25f); }
 __device__ inline uint32_t q4_low(uint32_t x) { return f16_codes(x & 0x000F000Fu, 32768.f, 0.015625f); }
 __device__ inline uint32_t q4_high(uint32_t x) { return f16_codes(x & 0x00F000F0u, 2048.f, 0.015625f); }
-constexpr float kCodeScale = 512.f;  // 2^9
+constexpr float kVScale = 512.f;          // 2^9
+constexpr float kKScale = 16777216.f;     // 2^24
+// -zero 2^-24 in both halves: of q8_0, of q4_0's low and high nibbles
+constexpr uint32_t kZero8 = 0x80808080u, kZero4Low = 0x80088008u, kZero4High = 0x80808080u;
 
 // Byte y0 of w0 and byte y1 of w1, each in a 16-bit half.
 __device__ inline uint32_t two_bytes(uint32_t w0, int y0, uint32_t w1, int y1) {
@@ -144,26 +170,114 @@ struct AttnShape {
   static constexpr bool kF16 = KIND != KV_BF16;
   static constexpr int NB = D / 32;
   // 32-bit words of a lane: K of one 16-key tile (four of the sixteen pair
-  // columns), V of one key (one column)
+  // columns), V of one key (one column), scales of four keys
   static constexpr int KW = KIND == KV_BF16 ? 4 * NB : KIND == KV_Q8_0 ? 2 * NB : NB;
   static constexpr int VW = KIND == KV_BF16 ? NB : KIND == KV_Q8_0 ? NB / 2 : (NB + 3) / 4;
-  static constexpr int SW = KIND == KV_BF16 ? 1 : 2 * NB;  // scales of four keys
+  static constexpr int SW = 2 * NB;
+
+  // A wave's LDS slot for a step of 32 keys: K codes, V codes [2][16][row],
+  // then the scales of K and V, [32][NB] fp16, each in whole 256 bytes.
+  static constexpr int kRow = int(kv_row_bytes(KIND, D));
+  static constexpr int kRC = kRow / 16;                        // 16-byte units of a row
+  static constexpr int kTile = 16 * kRow;
+  static constexpr int kScales = !kF16 ? 0 : NB <= 4 ? 256 : 512;
+  static constexpr int kSlot = 4 * kTile + 2 * kScales;
+  static constexpr int kKOff = 0, kVOff = 2 * kTile, kSkOff = 4 * kTile, kSvOff = kSkOff + kScales;
+  // slots of a wave: what lets two workgroups share a CU's 160 KB
+  static constexpr int kFit = 80 * 1024 / (kAttnWaves * kSlot);
+  static constexpr int kSlots = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
+  // transfers of K (or V) of a step
+  static constexpr int kCopies = kRow / 32 + kScales / 256;
+  static_assert(kCopies * (2 * kSlots + 1) <= 63, "vmcnt");
 };
 
-// What a lane has loaded of a step: lane (c, g) = (lane & 15, lane >> 4).
-template <int KIND, int D>
-struct StepRegs {
-  using S = AttnShape<KIND, D>;
-  uint32_t k[2][S::KW];   // key c of each tile, its elements 8g .. 8g + 7 of every block
-  uint32_t v[8][S::VW];   // keys 4g + i (tile 0), 4g + i - 4 (tile 1), column c
-  uint32_t sk[2][S::SW];  // scales of keys 4g .. 4g + 3 of each tile
-  uint32_t sv[2][S::SW];
-  int key;                // first key
-  bool there[2];          // whether a tile's page is in the cache
+// LDS position of a tile's 16-byte unit j of row c: the units of eight and of
+// sixteen consecutive rows at one j lie on different banks.
+template <int RC>
+__device__ inline int k_swizzle(int c) {
+  return RC >= 16 ? c : RC == 8 ? (c & 7) ^ (c >> 3) : RC == 4 ? ((c >> 1) & 3) ^ (c >> 3) : 0;
+}
+// LDS row of V's key c (and back): the rows 4g + i of the four g differ modulo 4.
+__device__ inline int v_row(int c) { return c ^ (c >> 2); }
+
+__device__ inline void dma4(const void* src, uint32_t dst) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+               "v"(src)
+               : "memory", "m0");
+#pragma clang diagnostic pop
+}
+template <int N>
+__device__ inline void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Waits for a step's K (or V) while `ahead` later steps, and for V the K of
+// one more, are on their way.  C copies for each of K and V.
+template <int C, int SLOTS, bool K>
+__device__ inline void wait_ahead(int ahead, bool more) {
+  if (more) {
+    wait_copies<2 * C * (SLOTS - 1) + C>();
+  } else if (ahead == SLOTS - 1) {
+    wait_copies<2 * C * (SLOTS - 1) + (K ? C : 0)>();
+  } else if constexpr (SLOTS > 1) {
+    wait_ahead<C, SLOTS - 1, K>(ahead, false);
+  }
+}
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Copies K (V = false) or V of the step's two 16-key tiles and their scales
+// into the slot at LDS address dst.  A page outside the cache is replaced by
+// page 0 (every key of it is masked).
+struct StepAt {
+  uint64_t codes[2], scales[2];  // offsets of the tiles in the buffers of K and V
 };
+template <int KIND, int D>
+__device__ inline StepAt step_at(const KvView& c, uint32_t head, int key, int32_t p0, int32_t p1) {
+  StepAt s;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int32_t page = t ? p1 : p0;
+    const uint64_t chunk = kv_chunk_at(c, kv_page_in(c, page) ? page : 0, head);
+    const uint32_t tok = uint32_t(key + 16 * t) & ((1u << c.shift) - 1);
+    s.codes[t] = chunk + kv_codes_at(KIND, D, tok);
+    s.scales[t] = chunk + kv_scales_at(KIND, D, c.shift, tok);
+  }
+  return s;
+}
+template <int KIND, int D, bool V>
+__device__ inline void copy_step(const KvView& c, const StepAt& from, uint32_t dst) {
+  using S = AttnShape<KIND, D>;
+  const int lane = threadIdx.x & 63;
+  const uint8_t* buf = V ? c.v : c.k;
+  const uint32_t codes = dst + (V ? S::kVOff : S::kKOff);
+  if constexpr (S::kRow >= 64) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < S::kRow / 64; ++j) {
+        const int row = j * (64 / S::kRC) + lane / S::kRC, unit = lane % S::kRC;
+        const uint32_t off = V ? v_row(row) * S::kRow + 16 * unit : row * S::kRow + 16 * (unit ^ k_swizzle<S::kRC>(row));
+        dma16_sv(buf + from.codes[t], off, codes + t * S::kTile + 1024 * j);
+      }
+  } else {  // both tiles in one transfer
+    static_assert(S::kRow >= 64 || S::kRow == 32, "row");
+    const int row = (lane & 31) / 2, unit = lane & 1;
+    const uint8_t* src = buf + (lane < 32 ? from.codes[0] : from.codes[1]);
+    dma16(src + (V ? v_row(row) : row) * S::kRow + 16 * unit, codes);
+  }
+  if constexpr (S::kF16) {
+    // 16 NB words over both tiles (NB = 2: the upper lanes repeat the lower)
+#pragma unroll
+    for (int j = 0; j < S::kScales / 256; ++j) {
+      const int w = (64 * j + lane) % (16 * S::NB), t = w / (8 * S::NB);
+      dma4(buf + (t ? from.scales[1] : from.scales[0]) + 4 * (w - t * 8 * S::NB), dst + (V ? S::kSvOff : S::kSkOff) + 256 * j);
+    }
+  }
+}
 
 template <int N>
-__device__ inline void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+__device__ inline void load_words(const uint8_t* p, uint32_t* w) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
@@ -178,46 +292,51 @@ __device__ inline void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
+// What a lane holds of a step, lane (c, g) = (lane & 15, lane >> 4).
 template <int KIND, int D>
-__device__ inline void load_step(StepRegs<KIND, D>& r, const KvView& c, uint32_t head, int key, int32_t p0,
-                                 int32_t p1) {
+struct StepRegs {
   using S = AttnShape<KIND, D>;
-  const uint32_t lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  r.key = key;
+  uint32_t k[2][S::KW];   // key c of each tile, its elements 8g .. 8g + 7 of every block
+  uint32_t v[8][S::VW];   // keys 4g + i (tile 0), 4g + i - 4 (tile 1), column c
+  uint32_t sk[2][S::SW];  // scales of keys 4g .. 4g + 3 of each tile
+  uint32_t sv[2][S::SW];
+  int key;                // first key
+  bool there[2];          // whether a tile's page is in the cache
+};
+
+template <int KIND, int D>
+__device__ inline void read_k(StepRegs<KIND, D>& r, const uint8_t* slot) {
+  using S = AttnShape<KIND, D>;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int32_t page = t ? p1 : p0;
-    r.there[t] = kv_page_in(c, page);
-    const uint64_t at = kv_chunk_at(c, r.there[t] ? page : 0, head);
-    const uint32_t tok = uint32_t(key + 16 * t) & ((1u << c.shift) - 1);
-    const uint8_t* kc = c.k + at + kv_codes_at(KIND, D, tok);
-    const uint8_t* vc = c.v + at + kv_codes_at(KIND, D, tok);
-    if constexpr (KIND == KV_BF16) {
-      // block b's elements 8g .. 8g + 7 are 16 bytes in place
-      uint32_t w[4];
+    const uint8_t* row = slot + S::kKOff + t * S::kTile + c * S::kRow;
+    const int z = k_swizzle<S::kRC>(c);
+    if constexpr (KIND == KV_BF16) {  // block b's elements 8g .. 8g + 7 are unit 4b + g
 #pragma unroll
-      for (int b = 0; b < S::NB; ++b) {
-        load_words(kc + col * (2 * D) + 64 * b + 16 * g, w);
+      for (int b = 0; b < S::NB; ++b) load_words<4>(row + 16 * ((4 * b + g) ^ z), &r.k[t][4 * b]);
+    } else if constexpr (S::KW >= 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.k[t][4 * b + i] = w[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load_words(vc + (4 * g + i) * (2 * D) + 4 * S::NB * col, r.v[4 * t + i]);
+      for (int j = 0; j < S::KW / 4; ++j) load_words<4>(row + 16 * ((g * (S::KW / 4) + j) ^ z), &r.k[t][4 * j]);
     } else {
-      const uint32_t row = kv_row_bytes(KIND, D);
-      load_words(kc + col * row + 4 * S::KW * g, r.k[t]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* p = vc + (4 * g + i) * row + (row / 16) * col;
-        if constexpr (KIND == KV_Q4_0 && D == 64)
-          r.v[4 * t + i][0] = *reinterpret_cast<const uint16_t*>(p);
-        else
-          load_words(p, r.v[4 * t + i]);
-      }
-      const uint32_t s = kv_scales_at(KIND, D, c.shift, tok + 4 * g);
-      load_words(c.k + at + s, r.sk[t]);
-      load_words(c.v + at + s, r.sv[t]);
+      load_words<S::KW>(row + 4 * S::KW * g, r.k[t]);
     }
+    if constexpr (S::kF16) load_words<S::SW>(slot + S::kSkOff + (16 * t + 4 * g) * 2 * S::NB, r.sk[t]);
+  }
+}
+template <int KIND, int D>
+__device__ inline void read_v(StepRegs<KIND, D>& r, const uint8_t* slot) {
+  using S = AttnShape<KIND, D>;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* p = slot + S::kVOff + t * S::kTile + v_row(4 * g + i) * S::kRow + S::kRC * c;
+      if constexpr (S::kRC == 2) r.v[4 * t + i][0] = *reinterpret_cast<const uint16_t*>(p);
+      else load_words<S::VW>(p, r.v[4 * t + i]);
+    }
+    if constexpr (S::kF16) load_words<S::SW>(slot + S::kSvOff + (16 * t + 4 * g) * 2 * S::NB, r.sv[t]);
   }
 }
 
@@ -234,15 +353,15 @@ __device__ inline u32x4 k_operand(const StepRegs<KIND, D>& r, int t, int b) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = r.k[t][i * (NB / 2) + (b >> 1)];
-      a[i] = q8_pair(two_bytes(w, 2 * (b & 1), w, 2 * (b & 1) + 1));
+      a[i] = two_bytes(w, 2 * (b & 1), w, 2 * (b & 1) + 1);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {  // bytes i NB + b and (i + 1) NB + b
       const int y0 = i * NB + b, y1 = (i + 1) * NB + b;
       const uint32_t x = two_bytes(r.k[t][y0 >> 2], y0 & 3, r.k[t][y1 >> 2], y1 & 3);
-      a[i] = q4_low(x);
-      a[i + 1] = q4_high(x);
+      a[i] = x & 0x000F000Fu;
+      a[i + 1] = x & 0x00F000F0u;
     }
   }
   return a;
@@ -289,6 +408,7 @@ __device__ inline float row_sum(float v) {
 template <int KIND, int D, int NT, int RT>
 struct WaveRows {
   uint32_t q[RT][D / 32][NT][4];
+  f32x4 zero[RT][KIND == KV_BF16 ? 1 : D / 32];  // of the codes, times the row's q
   f32x4 o[RT][D / 16];
   float rs[RT];  // scores are acc * rs
   float M[RT], l[RT];
@@ -305,14 +425,11 @@ __device__ inline void raise(WaveRows<KIND, D, NT, RT>& w, int rt, float m) {
   for (int n = 0; n < D / 16; ++n) w.o[rt][n] *= f;
 }
 
-template <int KIND, int D, int NT, int RT, bool EDGE>
-__device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& r, int ctx, int keys) {
+// Scores of the row with the lane's eight keys.
+template <int KIND, int D, int NT, int RT>
+__device__ inline void do_scores(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& r, float (&s)[RT][8]) {
   using S = AttnShape<KIND, D>;
   constexpr int NB = S::NB;
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-
-  // scores of the row with the lane's eight keys
-  float s[RT][8];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     f32x4 acc[RT];
@@ -323,7 +440,7 @@ __device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& 
       const u32x4 a = k_operand<KIND, D>(r, t, b);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        f32x4 x = KIND == KV_BF16 ? acc[rt] : f32x4{0.f, 0.f, 0.f, 0.f};
+        f32x4 x = KIND == KV_BF16 ? acc[rt] : w.zero[rt][b];
 #pragma unroll
         for (int i = NT - 1; i >= 0; --i)
           x = mfma<S::kF16>(a, u32x4{w.q[rt][b][i][0], w.q[rt][b][i][1], w.q[rt][b][i][2], w.q[rt][b][i][3]}, x);
@@ -344,6 +461,16 @@ __device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& 
       for (int i = 0; i < 4; ++i) s[rt][4 * t + i] = acc[rt][i] * w.rs[rt];
   }
 
+}
+
+// The softmax's step and the sums with V.  EDGE: keys that are not there, or
+// that not every row sees.
+template <int KIND, int D, int NT, int RT, bool EDGE>
+__device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& r, float (&s)[RT][8], int ctx,
+                                 int keys, const uint8_t* slot) {
+  using S = AttnShape<KIND, D>;
+  constexpr int NB = S::NB;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
   // keys that the row does not see
   uint32_t seen[RT];  // bit i: the lane's key i
   if constexpr (EDGE) {
@@ -376,19 +503,24 @@ __device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& 
           big = any && h < 0x7C00u && h > big ? h : big;
         }
       }
-    } else {
+    } else {  // every row sees all: the scales spread over the lanes
+      const uint32_t* sv = reinterpret_cast<const uint32_t*>(slot + S::kSvOff);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < S::SW; ++i) {
-          const uint32_t h = max(r.sv[t][i] & 0x7FFFu, (r.sv[t][i] >> 16) & 0x7FFFu);
-          big = max(big, h);
-        }
+      for (int j = 0; j < S::kScales / 256; ++j) {
+        const uint32_t x = sv[64 * j + lane] & 0x7FFF7FFFu;
+        big = max(big, max(x & 0xFFFFu, x >> 16));
+      }
     }
     const float top = h2f(big);
     if (__ballot(!(top <= pow2(w.be)))) {
       // the next power of two and two bits of room; at most 2^18 (fp16's largest)
       float t = row_max(top);
+      if constexpr (!EDGE) {
+        t = fmaxf(t, dpp_f<SKG_DPP_QUAD_XOR1>(t));
+        t = fmaxf(t, dpp_f<SKG_DPP_QUAD_XOR2>(t));
+        t = fmaxf(t, dpp_f<SKG_DPP_ROW_HALF_MIRROR>(t));
+        t = fmaxf(t, dpp_f<SKG_DPP_ROW_MIRROR>(t));
+      }
       t = t < 65504.f ? t : 65504.f;
       const int be = max(w.be, int(__builtin_bit_cast(uint32_t, t) >> 23) - 127 + 3);
       const float up = float(be - w.be);
@@ -426,8 +558,8 @@ __device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& 
 
   if constexpr (KIND == KV_BF16) {
     if constexpr (EDGE) {
-      // a value that no row sees may be anything: zero; one that some rows see
-      // may be infinite or NaN, which must not reach the others through 0 * v
+      // a value that is not there may be anything: zero; one that some rows
+      // see may be infinite or NaN, which must not reach the others as 0 * v
       uint32_t bad = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -441,36 +573,33 @@ __device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& 
         }
       }
       if (__ballot(bad != 0)) {
-        // row by row, with the values that the row does not see at zero
-        for (int row = 0; row < 16; ++row) {
+        // The sums take zeros in their place; where a row sees one, which the
+        // product of "is not finite" and "is seen" counts, its sum becomes NaN.
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          const u32x4 x = v_operand<KIND, D>(r, n);
+          u32x4 odd;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            odd[i] = ((x[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) | ((x[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
+#pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            uint32_t pt[4][NT];
-            uint32_t vis = 0;
+            u32x4 see;
 #pragma unroll
-            for (int k = 0; k < RT; ++k)
-              if (k == rt) {
+            for (int i = 0; i < 4; ++i)
+              see[i] = ((seen[rt] >> (2 * i)) & 1 ? 0x3F80u : 0u) | ((seen[rt] >> (2 * i + 1)) & 1 ? 0x3F800000u : 0u);
+            const f32x4 count = mfma<false>(odd, see, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split_pair<false, NT>(s[k][2 * i], s[k][2 * i + 1], pt[i]);
-                vis = __shfl(seen[k], (lane & 48) | row, 64);
-              }
-            StepRegs<KIND, D> z = r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int j = 0; j < S::VW; ++j) z.v[i][j] = ((vis >> i) & 1) ? r.v[i][j] : 0;
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-              const u32x4 a = v_operand<KIND, D>(z, n);
-              f32x4 x{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int i = NT - 1; i >= 0; --i) x = mfma<false>(a, u32x4{pt[0][i], pt[1][i], pt[2][i], pt[3][i]}, x);
-#pragma unroll
-              for (int k = 0; k < RT; ++k)
-                if (k == rt && (lane & 15) == row) w.o[k][n] += x;
-            }
+            for (int i = 0; i < 4; ++i) w.o[rt][n][i] = count[i] > 0.f ? __builtin_nanf("") : w.o[rt][n][i];
           }
         }
-        return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < S::VW; ++j) {
+            const uint32_t x = r.v[i][j];
+            r.v[i][j] = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
+          }
       }
     }
     uint32_t pt[RT][4][NT];
@@ -493,16 +622,18 @@ __device__ inline void do_step(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& 
       const u32x4 a0 = v_operand<KIND, D>(r, 2 * b), a1 = v_operand<KIND, D>(r, 2 * b + 1);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t sw = r.sv[i >> 2][((i & 3) * NB + b) >> 1];
-          y[i] = __builtin_fmaf((b & 1) ? f16_hi(sw) : f16_lo(sw), s[rt][i], 0.f);
-          if constexpr (EDGE) y[i] = ((seen[rt] >> i) & 1) ? y[i] : 0.f;  // an unseen key's scale may be NaN
-        }
         uint32_t pt[4][NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_pair<true, NT>(y[2 * i], y[2 * i + 1], pt[i]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t sw[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = 2 * i + j;
+            sw[j] = r.sv[k >> 2][((k & 3) * NB + b) >> 1];
+            if constexpr (EDGE) sw[j] = ((seen[rt] >> k) & 1) ? sw[j] : 0u;  // an unseen key's scale may be NaN
+          }
+          scaled_pair<NT>(s[rt][2 * i], s[rt][2 * i + 1], sw[0], sw[1], b & 1, pt[i]);
+        }
 #pragma unroll
         for (int i = NT - 1; i >= 0; --i) {
           const u32x4 p{pt[0][i], pt[1][i], pt[2][i], pt[3][i]};
@@ -552,7 +683,7 @@ __device__ inline void load_rows(WaveRows<KIND, D, NT, RT>& w, const TreeArgs& a
       int e = int((__builtin_bit_cast(uint32_t, amax) >> 23) & 255);  // |q| < 2^(e - 126)
       e = e < 40 ? 40 : (e > 220 ? 220 : e);
       to = __builtin_bit_cast(float, uint32_t(127 + 14 - (e - 126)) << 23);
-      w.rs[rt] *= kCodeScale * __builtin_bit_cast(float, uint32_t(127 - 14 + (e - 126)) << 23);
+      w.rs[rt] *= kKScale * __builtin_bit_cast(float, uint32_t(127 - 14 + (e - 126)) << 23);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -561,10 +692,22 @@ __device__ inline void load_rows(WaveRows<KIND, D, NT, RT>& w, const TreeArgs& a
         // q4_0's operand order: 0 2 1 3 4 6 5 7
         const int i0 = KIND == KV_Q4_0 ? 4 * (j >> 1) + (j & 1) : 2 * j, i1 = KIND == KV_Q4_0 ? i0 + 2 : 2 * j + 1;
         uint32_t t[NT];
-        split_pair<F16, NT>(x[b][i0] * to, x[b][i1] * to, t);
+        const float f = KIND == KV_Q4_0 && (j & 1) ? to * 0.0625f : to;  // against high nibbles
+        split_pair<F16, NT>(x[b][i0] * f, x[b][i1] * f, t);
 #pragma unroll
         for (int k = 0; k < NT; ++k) w.q[rt][b][k][j] = t[k];
       }
+    if constexpr (F16) {
+      const u32x4 z = KIND == KV_Q8_0 ? u32x4{kZero8, kZero8, kZero8, kZero8}
+                                      : u32x4{kZero4Low, kZero4High, kZero4Low, kZero4High};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        w.zero[rt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = NT - 1; k >= 0; --k)
+          w.zero[rt][b] = mfma<true>(z, u32x4{w.q[rt][b][k][0], w.q[rt][b][k][1], w.q[rt][b][k][2], w.q[rt][b][k][3]}, w.zero[rt][b]);
+      }
+    }
     w.mask[rt] = !is ? 0 : a.mask ? a.mask[sp.t0 + i] : ~uint64_t(0) >> (63 - i);
     w.M[rt] = kNoMax;
     w.l[rt] = 0.f;
@@ -623,10 +766,13 @@ __device__ inline void put_out(const TreeArgs& a, int64_t tok, int64_t at, const
 }
 
 template <class T, int KIND, int D, int NT, int RT>
-__global__ __launch_bounds__(kAttnThreads, (RT == 1 && D <= 128) ? 2 : 1) void tree_attn_kernel(TreeArgs a) {
+__global__ __launch_bounds__(kAttnThreads, (RT * D <= 256 && AttnShape<KIND, D>::kFit >= 1) ? 2 : 1) void tree_attn_kernel(TreeArgs a) {
+  using S = AttnShape<KIND, D>;
   constexpr int C = D < 128 ? D : 128;                       // elements joined at a time
   constexpr int EPT = 16 * C / kAttnThreads;                 // of a thread
-  __shared__ __attribute__((aligned(16))) float obuf[kAttnWaves][16][C + 4];
+  constexpr int kRing = kAttnWaves * S::kSlots * S::kSlot, kJoin = kAttnWaves * 16 * (C + 4) * 4;
+  // the ring, and after the last step the waves' sums
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
   __shared__ float ml[kAttnWaves][RT][16][2];
   // heads fastest, then splits, rows and sequences
   unsigned id = blockIdx.x;
@@ -640,30 +786,79 @@ __global__ __launch_bounds__(kAttnThreads, (RT == 1 && D <= 128) ? 2 : 1) void t
   const int first = rg * 16 * RT, rows = sp.n * a.group;
   if (first >= rows) return;
   const int per = steps_per_split(sp.keys, a.splits);
-  const int begin = split * per, steps = (sp.keys + kStep - 1) / kStep;
-  if (a.splits > 1 && begin >= steps && split > 0) return;
-  const int end = begin + per < steps ? begin + per : steps;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int begin = split * per, steps = sp.keys / kStep + (sp.keys % kStep != 0);
+  if (begin >= steps && split > 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int left = (begin + per < steps ? begin + per : steps) - begin - wave;
+  const int n = left > 0 ? (left + kAttnWaves - 1) / kAttnWaves : 0;  // this wave's steps
+
+  // pages of the wave's next 32 steps, two tiles each, over its lanes
+  const int32_t* table = a.table + int64_t(seq) * a.width;
+  auto key_of = [&](int i) SKG_INL { return (begin + wave + i * kAttnWaves) * kStep; };
+  auto pages_of = [&](int i0) SKG_INL -> int32_t {
+    const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
+    return i < n && key < sp.keys ? table[key >> a.cache.shift] : -1;
+  };
+  int32_t pages = pages_of(0);
+  uint8_t* ring = lds + wave * (S::kSlots * S::kSlot);
+  const uint32_t ring_at = lds_addr(ring);
+  auto page = [&](int i, int t) SKG_INL { return __builtin_amdgcn_readlane(pages, 2 * (i & 31) + t); };
+  auto at_of = [&](int i) SKG_INL { return step_at<KIND, D>(a.cache, head, key_of(i), page(i, 0), page(i, 1)); };
 
   WaveRows<KIND, D, NT, RT> w;
   load_rows<T, KIND, D, NT, RT>(w, a, sp, head, first);
 
-  const int32_t* table = a.table + int64_t(seq) * a.width;
-  auto page = [&](int step, int t) SKG_INL -> int32_t {
-    const int key = step * kStep + 16 * t;
-    return step < end && key < sp.keys ? __builtin_amdgcn_readfirstlane(table[key >> a.cache.shift]) : -1;
+  auto there_of = [&](int i) SKG_INL -> uint32_t {
+    return uint32_t(kv_page_in(a.cache, page(i, 0))) | uint32_t(kv_page_in(a.cache, page(i, 1))) << 1;
   };
-  for (int step = begin + wave; step < end; step += kAttnWaves) {
+  uint32_t there = 0;
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i)
+    if (i < n) {
+      there |= there_of(i) << (2 * i);
+      const StepAt from = at_of(i);
+      copy_step<KIND, D, false>(a.cache, from, ring_at + i * S::kSlot);
+      copy_step<KIND, D, true>(a.cache, from, ring_at + i * S::kSlot);
+    }
+  int slot = 0;
+  uint32_t flags = there;  // the copied steps' pages in the cache, two bits each, oldest first
+  for (int i = 0; i < n; ++i) {
+    const int ahead = n - 1 - i < S::kSlots - 1 ? n - 1 - i : S::kSlots - 1;  // later steps on their way
+    const bool more = i + S::kSlots < n;
+    uint8_t* at = ring + slot * S::kSlot;
     StepRegs<KIND, D> r;
-    load_step<KIND, D>(r, a.cache, head, step * kStep, page(step, 0), page(step, 1));
-    if (step * kStep + kStep <= sp.ctx && r.there[0] && r.there[1])
-      do_step<KIND, D, NT, RT, false>(w, r, sp.ctx, sp.keys);
+    r.key = key_of(i);
+    r.there[0] = flags & 1;
+    r.there[1] = flags & 2;
+    flags >>= 2;
+    float s[RT][8];
+    StepAt next;
+    wait_ahead<S::kCopies, S::kSlots, true>(ahead, false);
+    read_k<KIND, D>(r, at);
+    do_scores<KIND, D, NT, RT>(w, r, s);
+    if (more) {
+      if (((i + S::kSlots) & 31) == 0) pages = pages_of(i + S::kSlots);
+      flags |= there_of(i + S::kSlots) << (2 * (S::kSlots - 1));
+      wait_lds();
+      next = at_of(i + S::kSlots);
+      copy_step<KIND, D, false>(a.cache, next, ring_at + slot * S::kSlot);
+    }
+    wait_ahead<S::kCopies, S::kSlots, false>(ahead, more);
+    read_v<KIND, D>(r, at);
+    if (r.key + kStep <= sp.ctx && r.there[0] && r.there[1])
+      do_values<KIND, D, NT, RT, false>(w, r, s, sp.ctx, sp.keys, at);
     else
-      do_step<KIND, D, NT, RT, true>(w, r, sp.ctx, sp.keys);
+      do_values<KIND, D, NT, RT, true>(w, r, s, sp.ctx, sp.keys, at);
+    if (more) {
+      wait_lds();
+      copy_step<KIND, D, true>(a.cache, next, ring_at + slot * S::kSlot);
+    }
+    slot = slot + 1 == S::kSlots ? 0 : slot + 1;
   }
 
   // join the waves
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  float(*obuf)[16][C + 4] = reinterpret_cast<float(*)[16][C + 4]>(lds);
+  const int c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const float l = row_sum(w.l[rt]);
@@ -709,7 +904,7 @@ __global__ __launch_bounds__(kAttnThreads, (RT == 1 && D <= 128) ? 2 : 1) void t
       const int i = is ? row / a.group : 0, hd = head * a.group + (is ? row % a.group : 0);
       const int64_t tok = sp.t0 + i;
       if (a.splits == 1) {
-        const float inv = l == 0.f ? 0.f : (KIND == KV_BF16 ? 1.f : kCodeScale) / l;
+        const float inv = l == 0.f ? 0.f : (KIND == KV_BF16 ? 1.f : kVScale) / l;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
         put_out<T, EPT>(a, tok, int64_t(hd) * D + h * C + je, y, is);

@@ -136,7 +136,7 @@ hipError_t launch_tree_attn(const TreeArgs& args, int kind, int D, skg_dtype dt,
     default: e = f32 ? tree_attn_q4_0_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_q4_0_bf16(a, D, p.rt, unsigned(grid), stream); break;
   }
   if (e != hipSuccess || p.splits == 1) return e;
-  const float unit = kind == KV_BF16 ? 1.f : kCodeScale;
+  const float unit = kind == KV_BF16 ? 1.f : kVScale;
   return f32 ? join_dim<float>(a, D, unit, stream) : join_dim<__bf16>(a, D, unit, stream);
 }
 
