@@ -431,8 +431,9 @@ skg_status skg_qkv_rope_store(const skg_kv_cache* cache, skg_dtype dtype, int64_
  * o  : rows of `dtype`, ldo elements apart, or NULL.
  * oq : Q8_1 blocks [T][hq * head_dim / 32], 4-byte aligned, or NULL: exactly
  *      skg_quantize_act_q8_1 of the binary32 o.  SKG_F32 only.
- * ws : skg_tree_attn_workspace(...) bytes, 16-byte aligned, contents not read;
- *      NULL if that is 0.  Calls that may run at the same time need one each.
+ * ws : skg_tree_attn_workspace(...) bytes, 256-byte aligned, contents not read
+ *      (NULL if that is 0).  Calls that may run at the same time need one each,
+ *      and so do captured calls whose graphs may.
  * Products of a key and a query, probabilities and sums keep binary32's
  * precision for SKG_F32 (terms of 11 or 8 bits each on the matrix cores) and one
  * fp16 or bf16 rounding of q and p for SKG_BF16; sums are binary32.  The result
@@ -444,8 +445,8 @@ skg_status skg_qkv_rope_store(const skg_kv_cache* cache, skg_dtype dtype, int64_
  * pointers, both outputs null, scale, unknown types, a short workspace, overlaps), SKG_E_ALIGN,
  * SKG_E_UNSUPPORTED (oq with SKG_BF16).
  */
-size_t skg_tree_attn_workspace(const skg_kv_cache* cache, int64_t T, int64_t n_seqs, int hq, int max_draft,
-                               int64_t width, int64_t max_kv);
+size_t skg_tree_attn_workspace(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, int64_t n_seqs, int hq,
+                               int max_draft, int64_t width, int64_t max_kv);
 skg_status skg_tree_attn(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, int64_t n_seqs, int hq,
                          int max_draft, const void* q, int64_t ldq, const int32_t* cu, const int32_t* ctx,
                          const int32_t* table, int64_t width, int64_t max_kv, const uint64_t* mask, float scale,

@@ -87,7 +87,7 @@ def _load() -> ctypes.CDLL:
         "skg_kv_store": (i32, [vp, i32, i64, vp, i64, vp, i64, vp, vp]),
         "skg_kv_load": (i32, [vp, i32, i64, vp, vp, i64, vp, i64, vp]),
         "skg_qkv_rope_store": (i32, [vp, i32, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
-        "skg_tree_attn_workspace": (sz, [vp, i64, i64, i32, i32, i64, i64]),
+        "skg_tree_attn_workspace": (sz, [vp, i32, i64, i64, i32, i32, i64, i64]),
         "skg_tree_attn": (i32, [vp, i32, i64, i64, i32, i32, vp, i64, vp, vp, vp, i64, i64, vp, ctypes.c_float,
                                 vp, i64, vp, vp, sz, vp]),
         "skg_debug_block_dots": (i32, [i32, i64, i64, i64, i64, vp, vp, vp, vp]),

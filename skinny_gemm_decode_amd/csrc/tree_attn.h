@@ -41,7 +41,7 @@ struct TreeArgs {
   uint8_t* o;   // or null
   int64_t ldo;  // bytes
   uint8_t* oq;  // or null
-  const int32_t* cu;  // or null: T / n_seqs each
+  const int32_t* cu;  // or null: per_seq tokens each
   const int32_t* ctx;
   const int32_t* table;
   int64_t width;
@@ -53,30 +53,112 @@ struct TreeArgs {
   int hq;
   int group;  // query heads of a cache head
   int max_draft;
-  int64_t blocks;  // Q8_1 blocks of a token's row
-  // how the work is split
-  int splits;      // workgroups along the keys; > 1: partial results in ws
-  int row_groups;  // workgroups along the rows
-  float* ws;       // [T * hq][splits][D] sums, then [T * hq][splits][2] (M, l)
+  // set by the launch
+  int64_t blocks;    // Q8_1 blocks of a token's row
+  int per_seq;       // T / n_seqs
+  int want;          // splits to make of all sequences' keys together; 0: each sequence is one
+  int row_groups;    // workgroups along a sequence's rows
+  int tile;          // rows of a workgroup
+  float* sums;       // partial results: [split][row group][head][tile][D]
+  float* ml;         // their M and l: [split][row group][head][tile][2]
 };
 
-constexpr int kAttnWaves = 4;
-constexpr int kAttnThreads = 64 * kAttnWaves;
-constexpr int kStep = 32;                 // keys of a wave's step
-constexpr int kMinSteps = 2 * kAttnWaves; // steps of a split at least
-
-// Steps of each split of a sequence of `keys` keys (the same in the kernel
-// that writes the partial results and in the one that joins them).
-__host__ __device__ inline int steps_per_split(int keys, int splits) {
-  const int steps = keys / kStep + (keys % kStep != 0);
-  const int per = (steps + splits - 1) / splits;
-  return per < kMinSteps ? kMinSteps : per;
-}
+constexpr int kStep = 32;           // keys of a step
+constexpr int kMinSteps = 8;        // steps of a split at least, where a sequence is split
+constexpr int kMaxSplitSeqs = 256;  // sequences that a launch may split
 
 __device__ inline KvSpan span_of(const TreeArgs& a, int b) {
-  const int64_t per = a.T / a.n_seqs;
-  const int32_t t0 = a.cu ? a.cu[b] : int32_t(b * per), t1 = a.cu ? a.cu[b + 1] : int32_t((b + 1) * per);
+  const int32_t t0 = a.cu ? a.cu[b] : b * a.per_seq, t1 = a.cu ? a.cu[b + 1] : (b + 1) * a.per_seq;
   return kv_span(a.ctx[b], t0, t1, a.T, a.max_draft, a.max_kv);
+}
+
+__device__ inline int wave_sum_int(int v) {
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) v += __shfl_xor(v, i, 64);
+  return v;
+}
+__device__ inline int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Splits are of equal length over all sequences: per = the steps of all of
+// them over the splits that are wanted, so a long sequence gets many and a
+// short one gets one, and a workgroup finds its own from the lengths, one lane
+// a sequence.
+struct Splits {  // of 64 sequences, one a lane
+  KvSpan sp;
+  int n, incl;  // splits of the sequence; of it and all before it
+};
+__device__ __forceinline__ Splits lane_span(const TreeArgs& a, int b) {
+  Splits s{KvSpan{0, 0, 0, 0}, 0, 0};
+  if (b < a.n_seqs) s.sp = span_of(a, b);
+  return s;
+}
+__device__ inline int steps_of(const KvSpan& sp) { return sp.keys / kStep + (sp.keys % kStep != 0); }
+// Steps of a split.
+__device__ __forceinline__ int split_steps(const TreeArgs& a, const Splits& first) {
+  int total = steps_of(first.sp);
+  if (a.n_seqs > 1) {
+#pragma unroll 1
+    for (int b = 64; b < a.n_seqs; b += 64) total += steps_of(lane_span(a, b + (threadIdx.x & 63)).sp);
+    total = wave_sum_int(total);
+  }
+  total = __builtin_amdgcn_readfirstlane(total);
+  const int per = total / a.want + (total % a.want != 0);
+  return per < kMinSteps ? kMinSteps : per;
+}
+__device__ __forceinline__ void count_splits(const TreeArgs& a, Splits& s, int per, int before) {
+  const int n = (steps_of(s.sp) + per - 1) / per;
+  s.n = s.sp.n == 0 ? 0 : n < 1 ? 1 : n;
+  int incl = s.n;
+  if (a.n_seqs > 1) {
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) {
+      const int x = __shfl_up(incl, i, 64);
+      if (int(threadIdx.x & 63) >= i) incl += x;
+    }
+  }
+  s.incl = before + incl;
+}
+
+// What a workgroup does: steps [begin, end) of a sequence, one of `splits`, of
+// which the first is split `base` of all.
+struct Unit {
+  KvSpan sp;
+  int seq, begin, end, splits, base;
+};
+// Split u of all (by_seq: the splits of sequence u); false if there is none.
+__device__ __forceinline__ bool find_unit(const TreeArgs& a, int u, Unit& w, bool by_seq = false) {
+  if (a.want == 0) {
+    w.seq = u;
+    w.sp = span_of(a, u);
+    w.begin = 0;
+    w.end = steps_of(w.sp);
+    w.splits = 1;
+    w.base = 0;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  Splits s = lane_span(a, lane);
+  const int per = split_steps(a, s);
+  int before = 0;  // splits of the sequences of earlier rounds
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.n_seqs; b0 += 64) {
+    if (b0) s = lane_span(a, b0 + lane);
+    count_splits(a, s, per, before);
+    const uint64_t hit = __ballot(by_seq ? b0 + lane == u : s.incl > u && s.n > 0);
+    if (hit) {
+      const int b = __builtin_ctzll(hit);
+      w.seq = b0 + b;
+      w.splits = lane_of(s.n, b);
+      w.base = lane_of(s.incl, b) - w.splits;
+      w.sp = KvSpan{lane_of(s.sp.t0, b), lane_of(s.sp.ctx, b), lane_of(s.sp.n, b), lane_of(s.sp.keys, b)};
+      w.begin = (u - w.base) * per;
+      const int all = steps_of(w.sp);
+      w.end = w.begin + per < all ? w.begin + per : all;
+      return true;
+    }
+    before = lane_of(s.incl, 63);
+  }
+  return false;
 }
 
 constexpr int kLazy = 4;          // a score may pass M by this much (a power of two) before M moves
@@ -165,7 +247,10 @@ __device__ inline uint32_t two_halves(uint32_t w0, uint32_t w1, int hi) {
   return __builtin_amdgcn_perm(w1, w0, hi ? 0x07060302u : 0x05040100u);
 }
 
-template <int KIND, int D>
+// NT terms of q and p; RT tiles of 16 rows a wave; W waves, which share the keys
+// of a split between them (each its own steps) or, with ROWS, the rows (all the
+// same steps, from one ring).
+template <int KIND, int D, int NT, int RT, int W, bool ROWS>
 struct AttnShape {
   static constexpr bool kF16 = KIND != KV_BF16;
   static constexpr int NB = D / 32;
@@ -175,20 +260,39 @@ struct AttnShape {
   static constexpr int VW = KIND == KV_BF16 ? NB : KIND == KV_Q8_0 ? NB / 2 : (NB + 3) / 4;
   static constexpr int SW = 2 * NB;
 
-  // A wave's LDS slot for a step of 32 keys: K codes, V codes [2][16][row],
-  // then the scales of K and V, [32][NB] fp16, each in whole 256 bytes.
+  // q: in registers, or in LDS where all waves have the same rows and their
+  // sums leave no room
+  static constexpr bool kQLds = !ROWS && (RT > 1 || D > 128);
+  static constexpr int kQBytes = kQLds ? RT * NB * NT * 1024 : 0;
+  // K's codes as subnormals, which need the row's zeros in registers; with
+  // several tiles the conversion serves all of them
+  static constexpr bool kSubnormal = kF16 && !kQLds && RT == 1;
+
+  // An LDS slot for a step of 32 keys: K codes, V codes [2][16][row], then the
+  // scales of K and V, [32][NB] fp16, each in whole 256 bytes.
   static constexpr int kRow = int(kv_row_bytes(KIND, D));
-  static constexpr int kRC = kRow / 16;                        // 16-byte units of a row
+  static constexpr int kRC = kRow / 16;  // 16-byte units of a row
   static constexpr int kTile = 16 * kRow;
   static constexpr int kScales = !kF16 ? 0 : NB <= 4 ? 256 : 512;
   static constexpr int kSlot = 4 * kTile + 2 * kScales;
   static constexpr int kKOff = 0, kVOff = 2 * kTile, kSkOff = 4 * kTile, kSvOff = kSkOff + kScales;
-  // slots of a wave: what lets two workgroups share a CU's 160 KB
-  static constexpr int kFit = 80 * 1024 / (kAttnWaves * kSlot);
+  // up to four slots where two workgroups (of four waves) still share a CU's 160 KB
+  static constexpr int kRings = ROWS ? 1 : W;
+  static constexpr int kFit = ((W == 4 ? 80 : 160) * 1024 - kQBytes) / (kRings * kSlot);
+  static constexpr int kPerCu = W == 4 && kFit >= 1 ? 2 : 1;
   static constexpr int kSlots = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
-  // transfers of K (or V) of a step
+  // transfers of a wave: of K (or V) of a step, or of its part of both
   static constexpr int kCopies = kRow / 32 + kScales / 256;
-  static_assert(kCopies * (2 * kSlots + 1) <= 63, "vmcnt");
+  static constexpr int kPart = (2 * kRow / 32 + W - 1) / W + kScales / 256;
+  static_assert(ROWS ? kPart * kSlots <= 63 && kSlots >= 2 : kCopies * (2 * kSlots + 1) <= 63, "vmcnt");
+
+  // LDS: the ring and q; after the last step the waves' sums, M and l
+  static constexpr int C = D < 128 ? D : 128;  // elements joined at a time
+  static constexpr int kRing = kRings * kSlots * kSlot;
+  static constexpr int kJoin = W * 16 * (C + 4) * 4;
+  static constexpr int kMl = ROWS ? 0 : W * RT * 16 * 2 * 4;
+  static constexpr int kLds = kRing + kQBytes > kJoin + kMl ? kRing + kQBytes : kJoin + kMl;
+  static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 // LDS position of a tile's 16-byte unit j of row c: the units of eight and of
@@ -245,9 +349,8 @@ __device__ inline StepAt step_at(const KvView& c, uint32_t head, int key, int32_
   }
   return s;
 }
-template <int KIND, int D, bool V>
+template <class S, int KIND, int D, bool V>
 __device__ inline void copy_step(const KvView& c, const StepAt& from, uint32_t dst) {
-  using S = AttnShape<KIND, D>;
   const int lane = threadIdx.x & 63;
   const uint8_t* buf = V ? c.v : c.k;
   const uint32_t codes = dst + (V ? S::kVOff : S::kKOff);
@@ -276,6 +379,46 @@ __device__ inline void copy_step(const KvView& c, const StepAt& from, uint32_t d
   }
 }
 
+// One wave's part of a step's copies, every wave as many: W shares of the 1 KB
+// transfers of K and V (where there are fewer, some are made twice), and the
+// scales of K by even and of V by odd waves.
+template <class S, int KIND, int D, int W>
+__device__ inline void copy_part(const KvView& c, const StepAt& from, uint32_t dst, int wave) {
+  const int lane = threadIdx.x & 63;
+  constexpr int kAll = 2 * S::kRow / 32, kEach = (kAll + W - 1) / W;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int x = (wave * kEach + j) % kAll;  // [V][transfer]
+    const bool v = x >= kAll / 2;
+    const uint8_t* buf = v ? c.v : c.k;
+    if constexpr (S::kRow >= 64) {
+      const int y = v ? x - kAll / 2 : x, t = y / (S::kRow / 64), i = y % (S::kRow / 64);
+      const int row = i * (64 / S::kRC) + lane / S::kRC, unit = lane % S::kRC;
+      const uint32_t off = v ? v_row(row) * S::kRow + 16 * unit : row * S::kRow + 16 * (unit ^ k_swizzle<S::kRC>(row));
+      dma16_sv(buf + (t ? from.codes[1] : from.codes[0]), off, dst + (v ? S::kVOff : S::kKOff) + t * S::kTile + 1024 * i);
+    } else {
+      const int row = (lane & 31) / 2, unit = lane & 1;
+      const uint8_t* src = buf + (lane < 32 ? from.codes[0] : from.codes[1]);
+      dma16(src + (v ? v_row(row) : row) * S::kRow + 16 * unit, dst + (v ? S::kVOff : S::kKOff));
+    }
+  }
+  if constexpr (S::kF16) {
+    const bool v = wave & 1;
+    const uint8_t* buf = v ? c.v : c.k;
+#pragma unroll
+    for (int j = 0; j < S::kScales / 256; ++j) {
+      const int w = (64 * j + lane) % (16 * S::NB), t = w / (8 * S::NB);
+      dma4(buf + (t ? from.scales[1] : from.scales[0]) + 4 * (w - t * 8 * S::NB), dst + (v ? S::kSvOff : S::kSkOff) + 256 * j);
+    }
+  }
+}
+// Waits until at most `steps` steps' parts of C copies are on their way.
+template <int C, int MOST>
+__device__ inline void wait_parts(int steps) {
+  if (steps >= MOST) wait_copies<C * MOST>();
+  else if constexpr (MOST > 0) wait_parts<C, MOST - 1>(steps);
+}
+
 template <int N>
 __device__ inline void load_words(const uint8_t* p, uint32_t* w) {
   if constexpr (N % 4 == 0) {
@@ -293,9 +436,8 @@ __device__ inline void load_words(const uint8_t* p, uint32_t* w) {
 }
 
 // What a lane holds of a step, lane (c, g) = (lane & 15, lane >> 4).
-template <int KIND, int D>
+template <class S>
 struct StepRegs {
-  using S = AttnShape<KIND, D>;
   uint32_t k[2][S::KW];   // key c of each tile, its elements 8g .. 8g + 7 of every block
   uint32_t v[8][S::VW];   // keys 4g + i (tile 0), 4g + i - 4 (tile 1), column c
   uint32_t sk[2][S::SW];  // scales of keys 4g .. 4g + 3 of each tile
@@ -304,9 +446,8 @@ struct StepRegs {
   bool there[2];          // whether a tile's page is in the cache
 };
 
-template <int KIND, int D>
-__device__ inline void read_k(StepRegs<KIND, D>& r, const uint8_t* slot) {
-  using S = AttnShape<KIND, D>;
+template <class S, int KIND>
+__device__ inline void read_k(StepRegs<S>& r, const uint8_t* slot) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -324,9 +465,8 @@ __device__ inline void read_k(StepRegs<KIND, D>& r, const uint8_t* slot) {
     if constexpr (S::kF16) load_words<S::SW>(slot + S::kSkOff + (16 * t + 4 * g) * 2 * S::NB, r.sk[t]);
   }
 }
-template <int KIND, int D>
-__device__ inline void read_v(StepRegs<KIND, D>& r, const uint8_t* slot) {
-  using S = AttnShape<KIND, D>;
+template <class S, int KIND>
+__device__ inline void read_v(StepRegs<S>& r, const uint8_t* slot) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -342,9 +482,8 @@ __device__ inline void read_v(StepRegs<KIND, D>& r, const uint8_t* slot) {
 
 // K operand of block b of tile t: elements 8g .. 8g + 7 of the block (for q4_0
 // in the order 0 2 1 3 4 6 5 7, see q_order).
-template <int KIND, int D>
-__device__ inline u32x4 k_operand(const StepRegs<KIND, D>& r, int t, int b) {
-  constexpr int NB = D / 32;
+template <class S, int KIND, int NB>
+__device__ inline u32x4 k_operand(const StepRegs<S>& r, int t, int b) {
   u32x4 a;
   if constexpr (KIND == KV_BF16) {
 #pragma unroll
@@ -353,15 +492,16 @@ __device__ inline u32x4 k_operand(const StepRegs<KIND, D>& r, int t, int b) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = r.k[t][i * (NB / 2) + (b >> 1)];
-      a[i] = two_bytes(w, 2 * (b & 1), w, 2 * (b & 1) + 1);
+      const uint32_t x = two_bytes(w, 2 * (b & 1), w, 2 * (b & 1) + 1);
+      a[i] = S::kSubnormal ? x : q8_pair(x);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {  // bytes i NB + b and (i + 1) NB + b
       const int y0 = i * NB + b, y1 = (i + 1) * NB + b;
       const uint32_t x = two_bytes(r.k[t][y0 >> 2], y0 & 3, r.k[t][y1 >> 2], y1 & 3);
-      a[i] = x & 0x000F000Fu;
-      a[i + 1] = x & 0x00F000F0u;
+      a[i] = S::kSubnormal ? x & 0x000F000Fu : q4_low(x);
+      a[i + 1] = S::kSubnormal ? x & 0x00F000F0u : q4_high(x);
     }
   }
   return a;
@@ -369,8 +509,8 @@ __device__ inline u32x4 k_operand(const StepRegs<KIND, D>& r, int t, int b) {
 
 // V operand: column element n of the lane's eight keys.  Quantised: n = 2 b + e;
 // bf16: element (D / 16) c + n.
-template <int KIND, int D>
-__device__ inline u32x4 v_operand(const StepRegs<KIND, D>& r, int n) {
+template <class S, int KIND>
+__device__ inline u32x4 v_operand(const StepRegs<S>& r, int n) {
   u32x4 a;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -386,12 +526,6 @@ __device__ inline u32x4 v_operand(const StepRegs<KIND, D>& r, int n) {
   return a;
 }
 
-// Element of the result that lane (., g) holds at [n][i].
-template <int KIND, int D>
-__device__ inline int o_element(int g, int n, int i) {
-  return KIND == KV_BF16 ? (D / 16) * (4 * g + i) + n : 32 * (n >> 1) + 2 * (4 * g + i) + (n & 1);
-}
-
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ inline float pow2(int e) { return __builtin_bit_cast(float, uint32_t(127 + e) << 23); }
 // Largest of the four lanes of a row.
@@ -405,19 +539,20 @@ __device__ inline float row_sum(float v) {
 }
 
 // A wave's rows: RT tiles of 16, lane & 15 each.
-template <int KIND, int D, int NT, int RT>
+template <class S, int D, int NT, int RT>
 struct WaveRows {
-  uint32_t q[RT][D / 32][NT][4];
-  f32x4 zero[RT][KIND == KV_BF16 ? 1 : D / 32];  // of the codes, times the row's q
+  uint32_t q[S::kQLds ? 1 : RT][D / 32][NT][4];
+  f32x4 zero[S::kSubnormal ? D / 32 : 1];  // of the codes, times the row's q
+  const uint8_t* q_lds;                    // [RT][NB][NT] operands of 64 lanes, 16 bytes each
   f32x4 o[RT][D / 16];
-  float rs[RT];  // scores are acc * rs
+  float rs[RT];  // scores are acc * rs, rs >= 0
   float M[RT], l[RT];
   int be;        // quantised: M's sigma allows for scales up to 2^be
   uint64_t mask[RT];
 };
 
-template <int KIND, int D, int NT, int RT>
-__device__ inline void raise(WaveRows<KIND, D, NT, RT>& w, int rt, float m) {
+template <class W, int D>
+__device__ inline void raise(W& w, int rt, float m) {
   const float f = exp2_fast(w.M[rt] - m);
   w.M[rt] = m;
   w.l[rt] *= f;
@@ -425,54 +560,63 @@ __device__ inline void raise(WaveRows<KIND, D, NT, RT>& w, int rt, float m) {
   for (int n = 0; n < D / 16; ++n) w.o[rt][n] *= f;
 }
 
-// Scores of the row with the lane's eight keys.
-template <int KIND, int D, int NT, int RT>
-__device__ inline void do_scores(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& r, float (&s)[RT][8]) {
-  using S = AttnShape<KIND, D>;
+// Products of the row's q with the lane's eight keys, scaled by the keys' scales.
+template <class S, int KIND, int D, int NT, int RT>
+__device__ inline void do_scores(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, float (&s)[RT][8]) {
   constexpr int NB = S::NB;
+  f32x4 acc[2][RT];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    f32x4 acc[RT];
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int rt = 0; rt < RT; ++rt) acc[t][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const u32x4 a = k_operand<KIND, D>(r, t, b);
+  for (int b = 0; b < NB; ++b) {
+    u32x4 a[2];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        f32x4 x = KIND == KV_BF16 ? acc[rt] : w.zero[rt][b];
+    for (int t = 0; t < 2; ++t) a[t] = k_operand<S, KIND, NB>(r, t, b);
 #pragma unroll
-        for (int i = NT - 1; i >= 0; --i)
-          x = mfma<S::kF16>(a, u32x4{w.q[rt][b][i][0], w.q[rt][b][i][1], w.q[rt][b][i][2], w.q[rt][b][i][3]}, x);
-        if constexpr (KIND == KV_BF16) {
-          acc[rt] = x;
+    for (int rt = 0; rt < RT; ++rt) {
+      u32x4 q[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if constexpr (S::kQLds)
+          q[i] = *reinterpret_cast<const u32x4*>(w.q_lds + ((rt * NB + b) * NT + i) * 1024);
+        else
+          q[i] = u32x4{w.q[rt][b][i][0], w.q[rt][b][i][1], w.q[rt][b][i][2], w.q[rt][b][i][3]};
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (!S::kF16) x = acc[t][rt];
+        else if constexpr (S::kSubnormal) x = w.zero[b];
+#pragma unroll
+        for (int i = NT - 1; i >= 0; --i) x = mfma<S::kF16>(a[t], q[i], x);
+        if constexpr (!S::kF16) {
+          acc[t][rt] = x;
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // scale of key 4g + i, block b
             const uint32_t sw = r.sk[t][(i * NB + b) >> 1];
-            acc[rt][i] = __builtin_fmaf((b & 1) ? f16_hi(sw) : f16_lo(sw), x[i], acc[rt][i]);
+            acc[t][rt][i] = __builtin_fmaf((b & 1) ? f16_hi(sw) : f16_lo(sw), x[i], acc[t][rt][i]);
           }
         }
       }
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[rt][4 * t + i] = acc[rt][i] * w.rs[rt];
   }
-
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[rt][i] = acc[i >> 2][rt][i & 3];
 }
 
 // The softmax's step and the sums with V.  EDGE: keys that are not there, or
 // that not every row sees.
-template <int KIND, int D, int NT, int RT, bool EDGE>
-__device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>& r, float (&s)[RT][8], int ctx,
-                                 int keys, const uint8_t* slot) {
-  using S = AttnShape<KIND, D>;
+template <class S, int KIND, int D, int NT, int RT, bool EDGE>
+__device__ inline void do_values(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, float (&s)[RT][8], int ctx, int keys,
+                                 const uint8_t* slot) {
   constexpr int NB = S::NB;
   const int lane = threadIdx.x & 63, g = lane >> 4;
-  // keys that the row does not see
-  uint32_t seen[RT];  // bit i: the lane's key i
+  uint32_t seen[RT];  // bit i: whether the row sees the lane's key i
   if constexpr (EDGE) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -482,12 +626,11 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
         const int key = r.key + 16 * (i >> 2) + 4 * g + (i & 3), j = key - ctx;
         const bool in = r.there[i >> 2] && key < keys && (j < 0 || ((w.mask[rt] >> (j & 63)) & 1));
         seen[rt] |= uint32_t(in) << i;
-        s[rt][i] = in ? s[rt][i] : -INFINITY;
       }
     }
   }
 
-  // the largest scale of a value that is seen, and the scores, against M
+  // the largest scale of a value that is seen against M's sigma
   if constexpr (S::kF16) {
     uint32_t big = 0;
     if constexpr (EDGE) {
@@ -526,7 +669,7 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
       const float up = float(be - w.be);
       w.be = be;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) raise<KIND, D, NT, RT>(w, rt, w.M[rt] + up);
+      for (int rt = 0; rt < RT; ++rt) raise<WaveRows<S, D, NT, RT>, D>(w, rt, w.M[rt] + up);
     }
   }
   // sigma = 15 - kLazy - be: M = m - sigma, p <= 2^kLazy 2^sigma
@@ -536,23 +679,28 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
   float mx[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    mx[rt] = s[rt][0];
+    float m = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) mx[rt] = fmaxf(mx[rt], s[rt][i]);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (EDGE) m = ((seen[rt] >> i) & 1) ? fmaxf(m, s[rt][i]) : m;
+      else m = i ? fmaxf(m, s[rt][i]) : s[rt][i];
+    }
+    mx[rt] = EDGE && !seen[rt] ? -INFINITY : m * w.rs[rt];
     over |= mx[rt] > w.M[rt] + room;
   }
   if (__ballot(over)) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const float m = row_max(mx[rt]) - (room - float(kLazy));
-      raise<KIND, D, NT, RT>(w, rt, fmaxf(m, w.M[rt]));
+      raise<WaveRows<S, D, NT, RT>, D>(w, rt, fmaxf(m, w.M[rt]));
     }
   }
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s[rt][i] = exp2_fast(s[rt][i] - w.M[rt]);
+      const float p = exp2_fast(__builtin_fmaf(s[rt][i], w.rs[rt], -w.M[rt]));
+      s[rt][i] = EDGE && !((seen[rt] >> i) & 1) ? 0.f : p;
       w.l[rt] += s[rt][i];
     }
 
@@ -577,7 +725,7 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
         // product of "is not finite" and "is seen" counts, its sum becomes NaN.
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
-          const u32x4 x = v_operand<KIND, D>(r, n);
+          const u32x4 x = v_operand<S, KIND>(r, n);
           u32x4 odd;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -609,7 +757,7 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
       for (int i = 0; i < 4; ++i) split_pair<false, NT>(s[rt][2 * i], s[rt][2 * i + 1], pt[rt][i]);
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
-      const u32x4 a = v_operand<KIND, D>(r, n);
+      const u32x4 a = v_operand<S, KIND>(r, n);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -619,7 +767,7 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
   } else {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const u32x4 a0 = v_operand<KIND, D>(r, 2 * b), a1 = v_operand<KIND, D>(r, 2 * b + 1);
+      const u32x4 a0 = v_operand<S, KIND>(r, 2 * b), a1 = v_operand<S, KIND>(r, 2 * b + 1);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         uint32_t pt[4][NT];
@@ -645,156 +793,208 @@ __device__ inline void do_values(WaveRows<KIND, D, NT, RT>& w, StepRegs<KIND, D>
   }
 }
 
-// Queries of the wave's rows [first, first + 16 RT) of a sequence's n * group
-// into operand registers.  A row is scaled by a power of two into fp16's range.
+// Row `row` of a sequence: its token (from the first) and its query head.
+__device__ inline void row_of(const TreeArgs& a, int row, bool is, int& i, int& h) {
+  i = is ? int(unsigned(row) / unsigned(a.group)) : 0;
+  h = is ? row - i * a.group : 0;
+}
+
+// The raw q of row tile `first` .. + 15: lane (c, g) takes elements 8g .. 8g + 7
+// of every block of row c (zeros past the sequence's rows).
+template <class T, int D>
+struct RawRows {
+  u32x4 x[D / 32][8 / Elem<T>::kVec];
+};
+template <class T, int D>
+__device__ inline void fetch_rows(RawRows<T, D>& r, const TreeArgs& a, const KvSpan& sp, int head, int first) {
+  const int lane = threadIdx.x & 63, row = first + (lane & 15), g = lane >> 4;
+  const bool is = row < sp.n * a.group;
+  int i, h;
+  row_of(a, row, is, i, h);
+  const uint8_t* src = a.q + int64_t(sp.t0 + i) * a.ldq + (int64_t(head * a.group + h) * D + 8 * g) * int(sizeof(T));
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+    for (int u = 0; u < 8 / Elem<T>::kVec; ++u) {
+      r.x[b][u] = u32x4{0, 0, 0, 0};
+      if (is) r.x[b][u] = *reinterpret_cast<const u32x4*>(src + (32 * b + u * Elem<T>::kVec) * int(sizeof(T)));
+    }
+}
+
+// Operand terms of a tile's rows, scaled by a power of two into fp16's range;
+// put(b, k, words) stores them.  Returns the scores' factor (>= 0: a negative
+// scale turns q).
+template <class T, class S, int KIND, int D, int NT, class Put>
+__device__ inline float convert_rows(const RawRows<T, D>& raw, float scale, Put&& put) {
+  constexpr int NB = D / 32, V = Elem<T>::kVec;
+  float x[NB][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int u = 0; u < 8 / V; ++u) {
+      float y[V];
+      Elem<T>::unpack(raw.x[b][u], y);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[b][u * V + j] = y[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[b][j]));
+  }
+  float to = scale < 0.f ? -1.f : 1.f;
+  float rs = fabsf(scale) * 1.44269504f;
+  if constexpr (S::kF16) {
+    amax = row_max(amax);
+    int e = int((__builtin_bit_cast(uint32_t, amax) >> 23) & 255);  // |q| < 2^(e - 126)
+    e = e < 40 ? 40 : (e > 220 ? 220 : e);
+    to *= pow2(14 - (e - 126));
+    rs *= (S::kSubnormal ? kKScale : kVScale) * pow2(e - 126 - 14);
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    uint32_t w[NT][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // q4_0's operand order: 0 2 1 3 4 6 5 7
+      const int i0 = KIND == KV_Q4_0 ? 4 * (j >> 1) + (j & 1) : 2 * j, i1 = KIND == KV_Q4_0 ? i0 + 2 : 2 * j + 1;
+      const float f = KIND == KV_Q4_0 && S::kSubnormal && (j & 1) ? to * 0.0625f : to;  // against high nibbles
+      uint32_t t[NT];
+      split_pair<S::kF16, NT>(x[b][i0] * f, x[b][i1] * f, t);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) w[k][j] = t[k];
+    }
+#pragma unroll
+    for (int k = 0; k < NT; ++k) put(b, k, w[k]);
+  }
+  return rs;
+}
+
+// Sixteen lanes hold a row's elements in the joins: lane t of them has 32 k + 2 t
+// and the next of each 32-element block k, so that every store of theirs is
+// contiguous and a Q8_1 block lies in one 16-lane row.
+//
+// The blocks from element `at` of a token's row, in float32, bf16 or as Q8_1.
+// Every lane executes it; `is` stores.
+template <class T, int BLOCKS>
+__device__ inline void put_out(const TreeArgs& a, int64_t tok, int64_t at, const float (&y)[2 * BLOCKS], bool is) {
+  const int t = threadIdx.x & 15;
+  if (a.o && is) {
+    uint8_t* dst = a.o + tok * a.ldo + (at + 2 * t) * int(sizeof(T));
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k) Elem<T>::put_pair(dst + 32 * k * sizeof(T), y[2 * k], y[2 * k + 1]);
+  }
+  if constexpr (sizeof(T) == 4) {
+    if (a.oq) {
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        float am = fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1]));
+        am = fmaxf(am, dpp_f<SKG_DPP_QUAD_XOR1>(am));
+        am = fmaxf(am, dpp_f<SKG_DPP_QUAD_XOR2>(am));
+        am = fmaxf(am, dpp_f<SKG_DPP_ROW_HALF_MIRROR>(am));
+        am = fmaxf(am, dpp_f<SKG_DPP_ROW_MIRROR>(am));
+        const float d = q8_1_d(am), id = q8_1_id(d);
+        const int q0 = q8_1_code(y[2 * k], id), q1 = q8_1_code(y[2 * k + 1], id);
+        int sum = q0 + q1;
+        sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_QUAD_XOR1, 0xF, 0xF, false);
+        sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_QUAD_XOR2, 0xF, 0xF, false);
+        sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_ROW_HALF_MIRROR, 0xF, 0xF, false);
+        sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_ROW_MIRROR, 0xF, 0xF, false);
+        if (is) {
+          uint8_t* dst = a.oq + (tok * a.blocks + at / QK + k) * 36;
+          reinterpret_cast<uint16_t*>(dst + 4)[t] = uint16_t((q0 & 0xFF) | (q1 & 0xFF) << 8);
+          if (t == 0) *reinterpret_cast<uint32_t*>(dst) = q8_1_d16(d) | (q8_1_s16(d, sum) << 16);
+        }
+      }
+    }
+  }
+}
+
+// o = y / l (nothing seen: 0) to the outputs.
+template <class T, int BLOCKS>
+__device__ inline void finish(const TreeArgs& a, int64_t tok, int64_t at, float (&y)[2 * BLOCKS], float l, float unit, bool is) {
+  const float inv = unit / l;
+#pragma unroll
+  for (int j = 0; j < 2 * BLOCKS; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
+  put_out<T, BLOCKS>(a, tok, at, y, is);
+}
+
+// The products' initial values: minus the zero of the codes times the row's q.
+template <class S, int KIND, int NB, int NT, class W>
+__device__ inline void fill_zero(W& w) {
+  const u32x4 z = KIND == KV_Q8_0 ? u32x4{kZero8, kZero8, kZero8, kZero8} : u32x4{kZero4Low, kZero4High, kZero4Low, kZero4High};
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    w.zero[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = NT - 1; k >= 0; --k)
+      w.zero[b] = mfma<true>(z, u32x4{w.q[0][b][k][0], w.q[0][b][k][1], w.q[0][b][k][2], w.q[0][b][k][3]}, w.zero[b]);
+  }
+}
+
+// A wave's sums of a row tile, elements h C .. h C + C - 1, to LDS [16][C + 4].
+template <class S, int KIND, int D>
+__device__ inline void put_tile(const f32x4 (&o)[D / 16], float (*obuf)[S::C + 4], int c, int g, int h) {
+  constexpr int C = S::C;
+  if constexpr (KIND == KV_BF16) {  // element (D / 16) (4g + i) + n at [n][i]
+    constexpr int W = D / 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = W * (4 * g + i);
+      if (e / C == h) {
+#pragma unroll
+        for (int m = 0; m < W; m += 4)
+          *reinterpret_cast<f32x4*>(&obuf[c][e % C + m]) = f32x4{o[m][i], o[m + 1][i], o[m + 2][i], o[m + 3][i]};
+      }
+    }
+  } else {  // element 32 b + 8 g + 2 i + e at [2b + e][i]
+#pragma unroll
+    for (int b = 0; b < C / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const int n = 2 * (h * (C / 32) + b);
+        *reinterpret_cast<f32x4*>(&obuf[c][32 * b + 8 * g + 2 * i]) = f32x4{o[n][i], o[n + 1][i], o[n][i + 1], o[n + 1][i + 1]};
+      }
+  }
+}
+
+// Up to 16 RT rows a workgroup: its waves take every fourth step each and join
+// their sums at the end.  For few rows this is bound by the cache's bytes.
 template <class T, int KIND, int D, int NT, int RT>
-__device__ inline void load_rows(WaveRows<KIND, D, NT, RT>& w, const TreeArgs& a, const KvSpan& sp, int head, int first) {
-  constexpr bool F16 = KIND != KV_BF16;
-  constexpr int NB = D / 32;
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int rows = sp.n * a.group;
+__global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)) void tree_attn_kernel(TreeArgs a) {
+  using S = AttnShape<KIND, D, NT, RT, 4, false>;
+  constexpr int kWaves = 4;
+  constexpr int C = S::C, NB = S::NB;
+  constexpr int B = C / 32, EPT = 2 * B;  // blocks and elements of a thread in the joins
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  __shared__ float rs_lds[S::kQLds ? RT * 16 : 1];
+  const int head = blockIdx.x, rg = blockIdx.z;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c = lane & 15, g = lane >> 4;
+
+  Unit unit;
+  if (!find_unit(a, blockIdx.y, unit)) return;
+  const KvSpan sp = unit.sp;
+  const int first = rg * 16 * RT, rows = sp.n * a.group;
+  if (first >= rows) return;
+  const int left = unit.end - unit.begin - wave;
+  const int n = left > 0 ? (left + kWaves - 1) / kWaves : 0;  // this wave's steps
+
+  WaveRows<S, D, NT, RT> w;
+  // q first, then the pages, whose use waits for both
+  RawRows<T, D> raw;
+  const bool mine = !S::kQLds || wave < RT;
+  if (mine) fetch_rows<T, D>(raw, a, sp, head, first + (S::kQLds ? 16 * wave : 0));
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = first + 16 * rt + c;
     const bool is = row < rows;
-    const int i = is ? row / a.group : 0, h = is ? row % a.group : 0;
-    const uint8_t* src = a.q + int64_t(sp.t0 + i) * a.ldq + (int64_t(head * a.group + h) * D + 8 * g) * int(sizeof(T));
-    float x[NB][8];
-    float amax = 0.f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      constexpr int V = Elem<T>::kVec;
-#pragma unroll
-      for (int u = 0; u < 8 / V; ++u) {
-        float y[V];
-        u32x4 raw{0, 0, 0, 0};
-        if (is) raw = *reinterpret_cast<const u32x4*>(src + (32 * b + u * V) * int(sizeof(T)));
-        Elem<T>::unpack(raw, y);
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[b][u * V + j] = y[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[b][j]));
-    }
-    float to = 1.f;
-    w.rs[rt] = a.scale * 1.44269504f;
-    if constexpr (F16) {
-      amax = row_max(amax);
-      int e = int((__builtin_bit_cast(uint32_t, amax) >> 23) & 255);  // |q| < 2^(e - 126)
-      e = e < 40 ? 40 : (e > 220 ? 220 : e);
-      to = __builtin_bit_cast(float, uint32_t(127 + 14 - (e - 126)) << 23);
-      w.rs[rt] *= kKScale * __builtin_bit_cast(float, uint32_t(127 - 14 + (e - 126)) << 23);
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // q4_0's operand order: 0 2 1 3 4 6 5 7
-        const int i0 = KIND == KV_Q4_0 ? 4 * (j >> 1) + (j & 1) : 2 * j, i1 = KIND == KV_Q4_0 ? i0 + 2 : 2 * j + 1;
-        uint32_t t[NT];
-        const float f = KIND == KV_Q4_0 && (j & 1) ? to * 0.0625f : to;  // against high nibbles
-        split_pair<F16, NT>(x[b][i0] * f, x[b][i1] * f, t);
-#pragma unroll
-        for (int k = 0; k < NT; ++k) w.q[rt][b][k][j] = t[k];
-      }
-    if constexpr (F16) {
-      const u32x4 z = KIND == KV_Q8_0 ? u32x4{kZero8, kZero8, kZero8, kZero8}
-                                      : u32x4{kZero4Low, kZero4High, kZero4Low, kZero4High};
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        w.zero[rt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = NT - 1; k >= 0; --k)
-          w.zero[rt][b] = mfma<true>(z, u32x4{w.q[rt][b][k][0], w.q[rt][b][k][1], w.q[rt][b][k][2], w.q[rt][b][k][3]}, w.zero[rt][b]);
-      }
-    }
+    int i, h;
+    row_of(a, row, is, i, h);
     w.mask[rt] = !is ? 0 : a.mask ? a.mask[sp.t0 + i] : ~uint64_t(0) >> (63 - i);
-    w.M[rt] = kNoMax;
-    w.l[rt] = 0.f;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) w.o[rt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  w.be = -40;
-}
-
-// EPT consecutive elements of a token's row, from `at`, in float32, bf16 or as Q8_1 (lanes of a
-// 32-element block adjacent).  Every lane executes it; `is` stores.
-template <class T, int EPT>
-__device__ inline void put_out(const TreeArgs& a, int64_t tok, int64_t at, const float (&y)[EPT], bool is) {
-  if (a.o && is) {
-    uint8_t* dst = a.o + tok * a.ldo + at * int(sizeof(T));
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < EPT; i += 4) reinterpret_cast<f32x4*>(dst)[i / 4] = f32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
-    } else {
-      uint32_t u[EPT / 2];
-#pragma unroll
-      for (int i = 0; i < EPT / 2; ++i) u[i] = bf16_pair(y[2 * i], y[2 * i + 1]);
-      if constexpr (EPT == 8) *reinterpret_cast<u32x4*>(dst) = u32x4{u[0], u[1], u[2], u[3]};
-      else *reinterpret_cast<uint2*>(dst) = uint2{u[0], u[1]};
-    }
-  }
-  if constexpr (sizeof(T) == 4) {
-    if (a.oq) {
-      float am = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) am = fmaxf(am, fabsf(y[i]));
-      am = fmaxf(am, dpp_f<SKG_DPP_QUAD_XOR1>(am));
-      am = fmaxf(am, dpp_f<SKG_DPP_QUAD_XOR2>(am));
-      if constexpr (EPT == 4) am = fmaxf(am, dpp_f<SKG_DPP_ROW_HALF_MIRROR>(am));
-      const float d = q8_1_d(am), id = q8_1_id(d);
-      int sum = 0;
-      uint32_t word[EPT / 4];
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        const int q = q8_1_code(y[i], id);
-        sum += q;
-        word[i / 4] = (i % 4 ? word[i / 4] : 0u) | (uint32_t(q) & 0xFFu) << (8 * (i % 4));
-      }
-      sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_QUAD_XOR1, 0xF, 0xF, false);
-      sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_QUAD_XOR2, 0xF, 0xF, false);
-      if constexpr (EPT == 4) sum += __builtin_amdgcn_update_dpp(0, sum, SKG_DPP_ROW_HALF_MIRROR, 0xF, 0xF, false);
-      if (is) {
-        const int lane = int(at % QK) / EPT;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.oq) + (tok * a.blocks + at / QK) * 9;
-        if (lane == 0) dst[0] = q8_1_d16(d) | (q8_1_s16(d, sum) << 16);
-#pragma unroll
-        for (int i = 0; i < EPT / 4; ++i) dst[1 + lane * (EPT / 4) + i] = word[i];
-      }
-    }
-  }
-}
-
-template <class T, int KIND, int D, int NT, int RT>
-__global__ __launch_bounds__(kAttnThreads, (RT * D <= 256 && AttnShape<KIND, D>::kFit >= 1) ? 2 : 1) void tree_attn_kernel(TreeArgs a) {
-  using S = AttnShape<KIND, D>;
-  constexpr int C = D < 128 ? D : 128;                       // elements joined at a time
-  constexpr int EPT = 16 * C / kAttnThreads;                 // of a thread
-  constexpr int kRing = kAttnWaves * S::kSlots * S::kSlot, kJoin = kAttnWaves * 16 * (C + 4) * 4;
-  // the ring, and after the last step the waves' sums
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kJoin ? kRing : kJoin];
-  __shared__ float ml[kAttnWaves][RT][16][2];
-  // heads fastest, then splits, rows and sequences
-  unsigned id = blockIdx.x;
-  const int head = int(id % a.cache.heads);
-  id /= a.cache.heads;
-  const int split = int(id % unsigned(a.splits));
-  id /= unsigned(a.splits);
-  const int rg = int(id % unsigned(a.row_groups)), seq = int(id / unsigned(a.row_groups));
-
-  const KvSpan sp = span_of(a, seq);
-  const int first = rg * 16 * RT, rows = sp.n * a.group;
-  if (first >= rows) return;
-  const int per = steps_per_split(sp.keys, a.splits);
-  const int begin = split * per, steps = sp.keys / kStep + (sp.keys % kStep != 0);
-  if (begin >= steps && split > 0) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int left = (begin + per < steps ? begin + per : steps) - begin - wave;
-  const int n = left > 0 ? (left + kAttnWaves - 1) / kAttnWaves : 0;  // this wave's steps
-
   // pages of the wave's next 32 steps, two tiles each, over its lanes
-  const int32_t* table = a.table + int64_t(seq) * a.width;
-  auto key_of = [&](int i) SKG_INL { return (begin + wave + i * kAttnWaves) * kStep; };
+  const int32_t* table = a.table + int64_t(unit.seq) * a.width;
+  auto key_of = [&](int i) SKG_INL { return (unit.begin + wave + i * kWaves) * kStep; };
   auto pages_of = [&](int i0) SKG_INL -> int32_t {
     const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
     return i < n && key < sp.keys ? table[key >> a.cache.shift] : -1;
@@ -802,31 +1002,59 @@ __global__ __launch_bounds__(kAttnThreads, (RT * D <= 256 && AttnShape<KIND, D>:
   int32_t pages = pages_of(0);
   uint8_t* ring = lds + wave * (S::kSlots * S::kSlot);
   const uint32_t ring_at = lds_addr(ring);
-  auto page = [&](int i, int t) SKG_INL { return __builtin_amdgcn_readlane(pages, 2 * (i & 31) + t); };
+  auto page = [&](int i, int t) SKG_INL { return lane_of(pages, 2 * (i & 31) + t); };
   auto at_of = [&](int i) SKG_INL { return step_at<KIND, D>(a.cache, head, key_of(i), page(i, 0), page(i, 1)); };
-
-  WaveRows<KIND, D, NT, RT> w;
-  load_rows<T, KIND, D, NT, RT>(w, a, sp, head, first);
-
   auto there_of = [&](int i) SKG_INL -> uint32_t {
     return uint32_t(kv_page_in(a.cache, page(i, 0))) | uint32_t(kv_page_in(a.cache, page(i, 1))) << 1;
   };
-  uint32_t there = 0;
+  uint32_t flags = 0;  // the copied steps' pages in the cache, two bits each, oldest first
+  auto copy_both = [&](int i) SKG_INL {
+    flags |= there_of(i) << (2 * i);
+    const StepAt from = at_of(i);
+    copy_step<S, KIND, D, false>(a.cache, from, ring_at + i * S::kSlot);
+    copy_step<S, KIND, D, true>(a.cache, from, ring_at + i * S::kSlot);
+  };
+  // one step's copies, and q's conversion before the others: their issue
+  // waits for room in the memory pipeline
+  if (n > 0) copy_both(0);
+
+  w.q_lds = lds + S::kRing + 16 * lane;
+  if (mine) {
+    const float rs = convert_rows<T, S, KIND, D, NT>(raw, a.scale, [&](int b, int k, const uint32_t(&x)[4]) SKG_INL {
+      if constexpr (S::kQLds) {
+        *reinterpret_cast<u32x4*>(lds + S::kRing + 16 * lane + ((wave * NB + b) * NT + k) * 1024) = u32x4{x[0], x[1], x[2], x[3]};
+      } else {
 #pragma unroll
-  for (int i = 0; i < S::kSlots; ++i)
-    if (i < n) {
-      there |= there_of(i) << (2 * i);
-      const StepAt from = at_of(i);
-      copy_step<KIND, D, false>(a.cache, from, ring_at + i * S::kSlot);
-      copy_step<KIND, D, true>(a.cache, from, ring_at + i * S::kSlot);
-    }
+        for (int j = 0; j < 4; ++j) w.q[0][b][k][j] = x[j];
+      }
+    });
+    if constexpr (S::kQLds) rs_lds[16 * wave + c] = rs;
+    else w.rs[0] = rs;
+  }
+#pragma unroll 1
+  for (int i = 1; i < S::kSlots && i < n; ++i) copy_both(i);
+  if constexpr (S::kSubnormal) fill_zero<S, KIND, NB, NT>(w);
+  if constexpr (S::kQLds) {
+    __syncthreads();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) w.rs[rt] = rs_lds[16 * rt + c];
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    w.M[rt] = kNoMax;
+    w.l[rt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) w.o[rt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  w.be = -40;
+
   int slot = 0;
-  uint32_t flags = there;  // the copied steps' pages in the cache, two bits each, oldest first
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int ahead = n - 1 - i < S::kSlots - 1 ? n - 1 - i : S::kSlots - 1;  // later steps on their way
     const bool more = i + S::kSlots < n;
     uint8_t* at = ring + slot * S::kSlot;
-    StepRegs<KIND, D> r;
+    StepRegs<S> r;
     r.key = key_of(i);
     r.there[0] = flags & 1;
     r.there[1] = flags & 2;
@@ -834,92 +1062,220 @@ __global__ __launch_bounds__(kAttnThreads, (RT * D <= 256 && AttnShape<KIND, D>:
     float s[RT][8];
     StepAt next;
     wait_ahead<S::kCopies, S::kSlots, true>(ahead, false);
-    read_k<KIND, D>(r, at);
-    do_scores<KIND, D, NT, RT>(w, r, s);
+    read_k<S, KIND>(r, at);
+    do_scores<S, KIND, D, NT, RT>(w, r, s);
     if (more) {
       if (((i + S::kSlots) & 31) == 0) pages = pages_of(i + S::kSlots);
       flags |= there_of(i + S::kSlots) << (2 * (S::kSlots - 1));
-      wait_lds();
       next = at_of(i + S::kSlots);
-      copy_step<KIND, D, false>(a.cache, next, ring_at + slot * S::kSlot);
+      wait_lds();
+      copy_step<S, KIND, D, false>(a.cache, next, ring_at + slot * S::kSlot);
     }
     wait_ahead<S::kCopies, S::kSlots, false>(ahead, more);
-    read_v<KIND, D>(r, at);
+    read_v<S, KIND>(r, at);
     if (r.key + kStep <= sp.ctx && r.there[0] && r.there[1])
-      do_values<KIND, D, NT, RT, false>(w, r, s, sp.ctx, sp.keys, at);
+      do_values<S, KIND, D, NT, RT, false>(w, r, s, sp.ctx, sp.keys, at);
     else
-      do_values<KIND, D, NT, RT, true>(w, r, s, sp.ctx, sp.keys, at);
+      do_values<S, KIND, D, NT, RT, true>(w, r, s, sp.ctx, sp.keys, at);
     if (more) {
       wait_lds();
-      copy_step<KIND, D, true>(a.cache, next, ring_at + slot * S::kSlot);
+      copy_step<S, KIND, D, true>(a.cache, next, ring_at + slot * S::kSlot);
     }
     slot = slot + 1 == S::kSlots ? 0 : slot + 1;
   }
 
-  // join the waves
+  // Join the waves: lane t of the sixteen of row jr sums elements 32 k + 2 t and
+  // the next.
   float(*obuf)[16][C + 4] = reinterpret_cast<float(*)[16][C + 4]>(lds);
-  const int c = lane & 15, g = lane >> 4;
+  float(*ml)[RT][16][2] = reinterpret_cast<float(*)[RT][16][2]>(lds + S::kJoin);
+  const int jr = threadIdx.x >> 4, je = 2 * (threadIdx.x & 15);
+  const bool whole = unit.splits == 1;
+  constexpr float kUnit = KIND == KV_BF16 ? 1.f : kVScale;
+  // this split's partial results
+  const int64_t at = (int64_t(blockIdx.y) * gridDim.z + rg) * gridDim.x + head;
+  float* sums = a.sums + at * (16 * RT * D);
+  float* sums_ml = a.ml + at * (16 * RT * 2);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const float l = row_sum(w.l[rt]);
-    if (g == 0) {
-      ml[wave][rt][c][0] = w.M[rt];
-      ml[wave][rt][c][1] = l;
-    }
-  }
-  const int jr = threadIdx.x / (C / EPT), je = (threadIdx.x % (C / EPT)) * EPT;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int h = 0; h < D / C; ++h) {
       __syncthreads();
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = o_element<KIND, D>(g, n, i);
-          if (e / C == h) obuf[wave][c][e % C] = w.o[rt][n][i];
-        }
+      if (g == 0 && h == 0) {
+        ml[wave][rt][c][0] = w.M[rt];
+        ml[wave][rt][c][1] = l;
+      }
+      put_tile<S, KIND, D>(w.o[rt], obuf[wave], c, g, h);
       __syncthreads();
-      float M = kNoMax, l = 0.f, f[kAttnWaves], y[EPT];
+      float M = kNoMax, lsum = 0.f, f[kWaves], y[EPT];
 #pragma unroll
-      for (int k = 0; k < kAttnWaves; ++k) M = fmaxf(M, ml[k][rt][jr][0]);
+      for (int k = 0; k < kWaves; ++k) M = fmaxf(M, ml[k][rt][jr][0]);
 #pragma unroll
-      for (int k = 0; k < kAttnWaves; ++k) {
+      for (int k = 0; k < kWaves; ++k) {
         f[k] = exp2_fast(ml[k][rt][jr][0] - M);
-        l = fmaf(f[k], ml[k][rt][jr][1], l);
+        lsum = fmaf(f[k], ml[k][rt][jr][1], lsum);
       }
 #pragma unroll
       for (int i = 0; i < EPT; ++i) y[i] = 0.f;
 #pragma unroll
-      for (int k = 0; k < kAttnWaves; ++k)
+      for (int k = 0; k < kWaves; ++k)
 #pragma unroll
-        for (int i = 0; i < EPT; i += 4) {
-          const f32x4 o = *reinterpret_cast<const f32x4*>(&obuf[k][jr][je + i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[i + j] = fmaf(f[k], o[j], y[i + j]);
+        for (int i = 0; i < B; ++i) {
+          const f32x2 o = *reinterpret_cast<const f32x2*>(&obuf[k][jr][32 * i + je]);
+          y[2 * i] = fmaf(f[k], o.x, y[2 * i]);
+          y[2 * i + 1] = fmaf(f[k], o.y, y[2 * i + 1]);
         }
       const int row = first + 16 * rt + jr;
       const bool is = row < rows;
-      const int i = is ? row / a.group : 0, hd = head * a.group + (is ? row % a.group : 0);
-      const int64_t tok = sp.t0 + i;
-      if (a.splits == 1) {
-        const float inv = l == 0.f ? 0.f : (KIND == KV_BF16 ? 1.f : kVScale) / l;
-#pragma unroll
-        for (int j = 0; j < EPT; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
-        put_out<T, EPT>(a, tok, int64_t(hd) * D + h * C + je, y, is);
+      if (whole) {
+        int i, hd;
+        row_of(a, row, is, i, hd);
+        finish<T, B>(a, sp.t0 + i, int64_t(head * a.group + hd) * D + h * C, y, lsum, kUnit, is);
       } else if (is) {
-        const int64_t at = (tok * a.hq + hd) * a.splits + split;
-        float* dst = a.ws + at * D + h * C + je;
+        float* dst = sums + (16 * rt + jr) * D + h * C + je;
 #pragma unroll
-        for (int j = 0; j < EPT; j += 4) *reinterpret_cast<f32x4*>(dst + j) = f32x4{y[j], y[j + 1], y[j + 2], y[j + 3]};
-        if (h == 0 && je == 0) {
-          float* m = a.ws + a.T * a.hq * int64_t(a.splits) * D + 2 * at;
-          m[0] = M;
-          m[1] = l;
+        for (int j = 0; j < B; ++j) *reinterpret_cast<f32x2*>(dst + 32 * j) = f32x2{y[2 * j], y[2 * j + 1]};
+        if (h == 0 && je == 0) *reinterpret_cast<f32x2*>(sums_ml + 2 * (16 * rt + jr)) = f32x2{M, lsum};
+      }
+    }
+  }
+}
+
+// Up to 16 RT W rows a workgroup: every wave its own, all waves the same steps
+// from a ring that they fill together, so the cache is read once for all of
+// them.  One barrier a step: past it the step's copies (each wave waits for its
+// own before it) are there and the slot of the step before is free.
+template <class T, int KIND, int D, int NT, int RT, int W>
+__global__ __launch_bounds__(64 * W, (W == 8 || D <= 128 ? 2 : 1)) void tree_attn_rows_kernel(TreeArgs a) {
+  using S = AttnShape<KIND, D, NT, RT, W, true>;
+  constexpr int C = S::C, NB = S::NB, B = C / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  const int head = blockIdx.x, rg = blockIdx.z;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c = lane & 15, g = lane >> 4;
+
+  Unit unit;
+  if (!find_unit(a, blockIdx.y, unit)) return;
+  const KvSpan sp = unit.sp;
+  const int rows = sp.n * a.group, group_first = rg * 16 * RT * W;
+  if (group_first >= rows) return;
+  const int first = group_first + 16 * RT * wave;
+  const int n = unit.end - unit.begin;
+
+  WaveRows<S, D, NT, RT> w;
+  RawRows<T, D> raw[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    fetch_rows<T, D>(raw[rt], a, sp, head, first + 16 * rt);
+    const int row = first + 16 * rt + c;
+    const bool is = row < rows;
+    int i, h;
+    row_of(a, row, is, i, h);
+    w.mask[rt] = !is ? 0 : a.mask ? a.mask[sp.t0 + i] : ~uint64_t(0) >> (63 - i);
+  }
+  const int32_t* table = a.table + int64_t(unit.seq) * a.width;
+  auto key_of = [&](int i) SKG_INL { return (unit.begin + i) * kStep; };
+  auto pages_of = [&](int i0) SKG_INL -> int32_t {
+    const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
+    return i < n && key < sp.keys ? table[key >> a.cache.shift] : -1;
+  };
+  int32_t pages = pages_of(0);
+  const uint32_t ring_at = lds_addr(lds);
+  auto page = [&](int i, int t) SKG_INL { return lane_of(pages, 2 * (i & 31) + t); };
+  uint32_t flags = 0;  // the copied steps' pages in the cache, two bits each, oldest first
+  auto copy = [&](int i, int slot, int at) SKG_INL {
+    const int32_t p0 = page(i, 0), p1 = page(i, 1);
+    flags |= (uint32_t(kv_page_in(a.cache, p0)) | uint32_t(kv_page_in(a.cache, p1)) << 1) << (2 * at);
+    copy_part<S, KIND, D, W>(a.cache, step_at<KIND, D>(a.cache, head, key_of(i), p0, p1), ring_at + slot * S::kSlot, wave);
+  };
+#pragma unroll 1
+  for (int i = 0; i < S::kSlots - 1 && i < n; ++i) copy(i, i, i);
+
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    w.rs[rt] = convert_rows<T, S, KIND, D, NT>(raw[rt], a.scale, [&](int b, int k, const uint32_t(&x)[4]) SKG_INL {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w.q[rt][b][k][j] = x[j];
+    });
+    w.M[rt] = kNoMax;
+    w.l[rt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) w.o[rt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  w.be = -40;
+  if constexpr (S::kSubnormal) fill_zero<S, KIND, NB, NT>(w);
+
+  int slot = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    wait_parts<S::kPart, S::kSlots - 2>(n - 1 - i);
+    wait_lds();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const int next = i + S::kSlots - 1;
+    if (next < n) {
+      if ((next & 31) == 0) pages = pages_of(next);
+      copy(next, slot == 0 ? S::kSlots - 1 : slot - 1, S::kSlots - 1);
+    }
+    const uint8_t* at = lds + slot * S::kSlot;
+    StepRegs<S> r;
+    r.key = key_of(i);
+    r.there[0] = flags & 1;
+    r.there[1] = flags & 2;
+    flags >>= 2;
+    if (first < rows) {  // a wave without rows copies only
+      float s[RT][8];
+      read_k<S, KIND>(r, at);
+      do_scores<S, KIND, D, NT, RT>(w, r, s);
+      read_v<S, KIND>(r, at);
+      if (r.key + kStep <= sp.ctx && r.there[0] && r.there[1])
+        do_values<S, KIND, D, NT, RT, false>(w, r, s, sp.ctx, sp.keys, at);
+      else
+        do_values<S, KIND, D, NT, RT, true>(w, r, s, sp.ctx, sp.keys, at);
+    }
+    slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+  }
+
+  // each wave's rows through its part of LDS, four rows of 16 lanes at a time
+  __syncthreads();
+  float(*obuf)[C + 4] = reinterpret_cast<float(*)[C + 4]>(lds) + 16 * wave;
+  const bool whole = unit.splits == 1;
+  constexpr float kUnit = KIND == KV_BF16 ? 1.f : kVScale;
+  const int64_t at = (int64_t(blockIdx.y) * gridDim.z + rg) * gridDim.x + head;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float l = row_sum(w.l[rt]);
+#pragma unroll
+    for (int h = 0; h < D / C; ++h) {
+      wait_lds();
+      put_tile<S, KIND, D>(w.o[rt], obuf, c, g, h);
+      wait_lds();
+#pragma unroll 1
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const int jr = 4 * i4 + g, je = 2 * c;  // row, elements 32 j + je
+        float y[2 * B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          const f32x2 o = *reinterpret_cast<const f32x2*>(&obuf[jr][32 * j + je]);
+          y[2 * j] = o.x;
+          y[2 * j + 1] = o.y;
+        }
+        const float M = __shfl(w.M[rt], jr, 64), lsum = __shfl(l, jr, 64);
+        const int local = 16 * (RT * wave + rt) + jr, row = group_first + local;
+        const bool is = row < rows;
+        if (whole) {
+          int i, hd;
+          row_of(a, row, is, i, hd);
+          finish<T, B>(a, sp.t0 + i, int64_t(head * a.group + hd) * D + h * C, y, lsum, kUnit, is);
+        } else if (is) {
+          float* dst = a.sums + (at * a.tile + local) * D + h * C + je;
+#pragma unroll
+          for (int j = 0; j < B; ++j) *reinterpret_cast<f32x2*>(dst + 32 * j) = f32x2{y[2 * j], y[2 * j + 1]};
+          if (h == 0 && je == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * (at * a.tile + local)) = f32x2{M, lsum};
         }
       }
     }
+  }
 }
 
 }  // namespace skg

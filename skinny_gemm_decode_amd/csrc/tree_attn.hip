@@ -1,4 +1,4 @@
-// How an attention call is split, and the join of its splits' partial results.
+// How an attention call is split, its launch, and the join of the splits.
 #include "tree_attn.h"
 #include "tree_attn_instances.h"
 
@@ -6,138 +6,198 @@ namespace skg {
 
 namespace {
 
-// Joins the splits of a row: with M* the largest M, o = sum 2^(M - M*) o_s and
-// l likewise.  A row's D / 8 threads of 8 elements are repeated over `par`
-// lanes of splits, which meet in LDS.
-template <class T, int D>
-__global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeArgs a, float unit, int par) {
-  constexpr int EPT = 8, kRow = D / EPT;   // threads of a row
-  constexpr int kSlots = 256 / kRow;       // rows times split lanes of a workgroup
-  __shared__ __attribute__((aligned(16))) float buf[kSlots][D];
-  __shared__ float ml[kSlots][2];
-  const int slot = threadIdx.x / kRow, e = (threadIdx.x % kRow) * EPT;
-  const int lane = slot % par, nrow = kSlots / par;
-  // rows (i, head) of sequence blockIdx.y
-  const KvSpan sp = span_of(a, blockIdx.y);
-  const int r = int(blockIdx.x) * nrow + slot / par;
-  const bool is = r < sp.n * a.hq;
-  if (int(blockIdx.x) * nrow >= sp.n * a.hq) return;  // uniform
-  const int64_t tok = sp.t0 + (is ? r / a.hq : 0);
-  const int hd = is ? r % a.hq : 0;
-  const int per = steps_per_split(sp.keys, a.splits);
-  const int steps = sp.keys / kStep + (sp.keys % kStep != 0);
-  int n = (steps + per - 1) / per;
-  n = n < 1 ? 1 : n;
-  const int64_t at = (tok * a.hq + hd) * a.splits;
-  const float* po = a.ws + at * D + e;
-  const float* pm = a.ws + a.T * a.hq * int64_t(a.splits) * D + 2 * at;
-  float M = kNoMax, l = 0.f, y[EPT];
+// Joins the splits of a row: with M* the largest M, o = sum 2^(M - M*) o_s, and
+// l likewise.  SUBS groups of 16 lanes take the splits in turn and meet by
+// shuffles and, with more than a wave's four, in LDS; the order is fixed.  It
+// is a launch of its own because the partial results then come through all
+// CUs: the last workgroup to arrive joining them (write-through stores and a
+// counter) took 3.3 us where this takes 3.9 with its launch at 16 splits of 8
+// rows, but 8 where this takes 5 at 64, and needed a workspace kept at zero.
+template <class T, int D, int SUBS>
+__global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeArgs a, float unit) {
+  constexpr int B = D / 32, kDeep = 4;
+  __shared__ __attribute__((aligned(16))) float buf[SUBS > 4 ? 4 : 1][D];
+  __shared__ float ml[4][2];
+  const int wave = threadIdx.x >> 6, je = 2 * (threadIdx.x & 15);
+  const int sub = SUBS > 4 ? threadIdx.x >> 4 : (threadIdx.x >> 4) & 3;
+  const int h = SUBS > 4 ? blockIdx.x : 4 * blockIdx.x + wave, i = blockIdx.y;
+  Unit unit_of;
+  if (!find_unit(a, blockIdx.z, unit_of, true)) return;
+  const KvSpan sp = unit_of.sp;
+  const int splits = unit_of.splits, before = unit_of.base;
+  if (i >= sp.n || splits <= 1 || h >= a.hq) return;  // uniform over a wave, with SUBS > 4 over the workgroup
+  const int row = i * a.group + h % a.group, head = h / a.group;
+  const int rg = row / a.tile, local = row - rg * a.tile;
+  const int64_t step = int64_t(a.row_groups) * a.cache.heads;
+  const int64_t at = ((before * step + int64_t(rg) * a.cache.heads + head) * a.tile + local);
+  const float* po = a.sums + at * D + je;
+  const float* pm = a.ml + 2 * at;
+  const int64_t so = step * a.tile * D, sm = step * a.tile * 2;
+  float M = kNoMax, l = 0.f, y[2 * B];
 #pragma unroll
-  for (int j = 0; j < EPT; ++j) y[j] = 0.f;
-  if (is)
-    for (int s = lane; s < n; s += par) {
-      const float ms = pm[2 * s], ls = pm[2 * s + 1];
-      const f32x4 o0 = *reinterpret_cast<const f32x4*>(po + int64_t(s) * D);
-      const f32x4 o1 = *reinterpret_cast<const f32x4*>(po + int64_t(s) * D + 4);
-      const float m = fmaxf(M, ms), f = exp2_fast(M - m), g = exp2_fast(ms - m);
-      M = m;
-      l = fmaf(l, f, ls * g);
+  for (int j = 0; j < 2 * B; ++j) y[j] = 0.f;
+#pragma unroll 1
+  for (int s0 = sub; s0 < splits; s0 += kDeep * SUBS) {
+    f32x2 m[kDeep], o[kDeep][B];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[j] = fmaf(y[j], f, o0[j] * g);
-        y[4 + j] = fmaf(y[4 + j], f, o1[j] * g);
+    for (int k = 0; k < kDeep; ++k) {
+      const int s = s0 + k * SUBS < splits ? s0 + k * SUBS : s0;
+      m[k] = *reinterpret_cast<const f32x2*>(pm + s * sm);
+#pragma unroll
+      for (int j = 0; j < B; ++j) o[k][j] = *reinterpret_cast<const f32x2*>(po + s * so + 32 * j);
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) top = fmaxf(top, m[k].x);
+    const float f = exp2_fast(M - top);
+    M = top;
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < 2 * B; ++j) y[j] *= f;
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const float e = s0 + k * SUBS < splits ? exp2_fast(m[k].x - M) : 0.f;
+      l = fmaf(m[k].y, e, l);
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        y[2 * j] = fmaf(o[k][j].x, e, y[2 * j]);
+        y[2 * j + 1] = fmaf(o[k][j].y, e, y[2 * j + 1]);
       }
     }
-  if (par > 1) {  // uniform
+  }
+  {  // the wave's four groups of lanes
+    const float top = row_max(M), e = exp2_fast(M - top);
+    M = top;
+    l = row_sum(l * e);
 #pragma unroll
-    for (int j = 0; j < EPT; j += 4) *reinterpret_cast<f32x4*>(&buf[slot][e + j]) = f32x4{y[j], y[j + 1], y[j + 2], y[j + 3]};
-    if (e == 0) {
-      ml[slot][0] = M;
-      ml[slot][1] = l;
+    for (int j = 0; j < 2 * B; ++j) y[j] = row_sum(y[j] * e);
+  }
+  if constexpr (SUBS > 4) {
+    if ((threadIdx.x & 63) < 16) {
+#pragma unroll
+      for (int j = 0; j < B; ++j) *reinterpret_cast<f32x2*>(&buf[wave][32 * j + je]) = f32x2{y[2 * j], y[2 * j + 1]};
+      ml[wave][0] = M;
+      ml[wave][1] = l;
     }
     __syncthreads();
-    const int first = slot - lane;
     M = kNoMax;
-    for (int s = 0; s < par; ++s) M = fmaxf(M, ml[first + s][0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) M = fmaxf(M, ml[k][0]);
     l = 0.f;
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) y[j] = 0.f;
-    for (int s = 0; s < par; ++s) {
-      const float f = exp2_fast(ml[first + s][0] - M);
-      l = fmaf(ml[first + s][1], f, l);
+    for (int j = 0; j < 2 * B; ++j) y[j] = 0.f;
 #pragma unroll
-      for (int j = 0; j < EPT; ++j) y[j] = fmaf(buf[first + s][e + j], f, y[j]);
+    for (int k = 0; k < 4; ++k) {
+      const float e = exp2_fast(ml[k][0] - M);
+      l = fmaf(ml[k][1], e, l);
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const f32x2 o = *reinterpret_cast<const f32x2*>(&buf[k][32 * j + je]);
+        y[2 * j] = fmaf(o.x, e, y[2 * j]);
+        y[2 * j + 1] = fmaf(o.y, e, y[2 * j + 1]);
+      }
     }
   }
-  const float inv = unit / l;
-#pragma unroll
-  for (int j = 0; j < EPT; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
-  put_out<T, EPT>(a, tok, int64_t(hd) * D + e, y, is && lane == 0);
+  finish<T, B>(a, sp.t0 + i, int64_t(h) * D, y, l, unit, sub == 0);
 }
 
 template <class T, int D>
-hipError_t join(const TreeArgs& a, float unit, hipStream_t stream) {
-  constexpr int kSlots = 256 / (D / 8);
-  int par = 1;
-  while (par < a.splits && par < kSlots) par *= 2;
-  const int nrow = kSlots / par;
-  const int64_t rows = int64_t(a.max_draft) * a.hq;
-  hipLaunchKernelGGL((tree_attn_join_kernel<T, D>), dim3(unsigned((rows + nrow - 1) / nrow), unsigned(a.n_seqs)),
-                     dim3(256), 0, stream, a, unit, par);
+hipError_t join(const TreeArgs& a, float unit, bool wide, hipStream_t stream) {
+  if (wide)
+    hipLaunchKernelGGL((tree_attn_join_kernel<T, D, 16>), dim3(unsigned(a.hq), unsigned(a.max_draft), unsigned(a.n_seqs)),
+                       dim3(256), 0, stream, a, unit);
+  else
+    hipLaunchKernelGGL((tree_attn_join_kernel<T, D, 4>), dim3(unsigned((a.hq + 3) / 4), unsigned(a.max_draft), unsigned(a.n_seqs)),
+                       dim3(256), 0, stream, a, unit);
   return hipGetLastError();
 }
 template <class T>
-hipError_t join_dim(const TreeArgs& a, int D, float unit, hipStream_t s) {
-  return D == 64 ? join<T, 64>(a, unit, s) : D == 128 ? join<T, 128>(a, unit, s) : join<T, 256>(a, unit, s);
+hipError_t join_dim(const TreeArgs& a, int D, float unit, bool wide, hipStream_t s) {
+  return D == 64 ? join<T, 64>(a, unit, wide, s) : D == 128 ? join<T, 128>(a, unit, wide, s) : join<T, 256>(a, unit, wide, s);
 }
 
 struct Plan {
-  int rt, row_groups, splits;
+  AttnForm form;
+  int row_groups, want;
+  int64_t slots;  // splits at most
+  bool wide;      // the join: 16 lanes groups a row, not four
+  size_t ml, bytes;
 };
 
-// Two row tiles of 16 a wave where there are more rows than one tile has: the
-// keys' conversion then serves both.  The keys are split until there are two
-// workgroups for each of 256 CUs, but none into less than two steps a wave.
-Plan plan(int heads, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
+// Up to 32 rows of a head: the waves share the keys.  More: they share the
+// rows, so that the cache is read once for 64, 128 or (one term a product,
+// two row tiles a wave) 256 of them; at D = 256 a row tile fills a wave's
+// registers, and only four waves have room.
+AttnForm form_of(int D, skg_dtype dt, int64_t rows) {
+  if (rows <= 16) return kKeys1;
+  if (rows <= 32 && D <= 128) return kKeys2;
+  if (rows <= 64 || D > 128) return kRows64;
+  if (rows <= 128 || dt == SKG_F32) return kRows128;
+  return kRows256;
+}
+constexpr int kTileOf[] = {16, 32, 64, 128, 256};
+
+// Splits: two workgroups of four waves (one of eight) for each of 256 CUs,
+// counted over all heads, row groups and sequences; where there are that many
+// without splitting, four times as many, so that long sequences do not stand
+// alone at the end.  More than 256 sequences are not split.
+Plan plan(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
   Plan p;
   const int64_t rows = int64_t(max_draft) * (hq / heads);
-  p.rt = rows <= 16 ? 1 : 2;
-  p.row_groups = int((rows + 16 * p.rt - 1) / (16 * p.rt));
-  const int64_t units = n_seqs * heads * p.row_groups, steps = (max_kv + kStep - 1) / kStep;
-  int64_t s = (512 + units - 1) / units;
-  const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
-  s = s < most ? s : most;
-  p.splits = int(s < 1 ? 1 : s);
+  p.form = form_of(D, dt, rows);
+  const int tile = kTileOf[p.form];
+  p.row_groups = int((rows + tile - 1) / tile);
+  const int64_t lanes = int64_t(heads) * p.row_groups;  // workgroups of a split
+  const int64_t steps = (max_kv + kStep - 1) / kStep, each = (steps + kMinSteps - 1) / kMinSteps;
+  int64_t want = 0;
+  if (n_seqs <= kMaxSplitSeqs && each > 1) {
+    const int64_t full = p.form >= kRows128 ? 256 : 512;
+    const int64_t fill = lanes * n_seqs <= full / 2 ? full : 4 * full;
+    want = fill / lanes - n_seqs / 2;
+    want = want < 1 ? 1 : want;
+  }
+  p.want = int(want);
+  p.slots = want ? (want + n_seqs < n_seqs * each ? want + n_seqs : n_seqs * each) : n_seqs;
+  const int64_t most = want < each ? want : each;  // splits of a sequence
+  p.wide = most > 4 && T * hq < 2048;
+  p.ml = p.bytes = 0;
+  if (want) {
+    const size_t part = size_t(p.slots) * size_t(lanes) * size_t(tile);
+    p.ml = (part * 2 * 4 + 255) & ~size_t(255);
+    p.bytes = p.ml + part * size_t(D) * 4;
+  }
   return p;
 }
 
 }  // namespace
 
-size_t tree_attn_workspace(int, int D, int heads, int64_t T, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
-  const Plan p = plan(heads, n_seqs, hq, max_draft, max_kv);
-  return p.splits == 1 ? 0 : size_t(T) * size_t(hq) * size_t(p.splits) * size_t(D + 2) * sizeof(float);
+size_t tree_attn_workspace(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft,
+                           int64_t max_kv) {
+  return plan(D, heads, dt, T, n_seqs, hq, max_draft, max_kv).bytes;
 }
 
 hipError_t launch_tree_attn(const TreeArgs& args, int kind, int D, skg_dtype dt, int heads, void* ws,
                             hipStream_t stream) {
   TreeArgs a = args;
-  const Plan p = plan(heads, a.n_seqs, a.hq, a.max_draft, a.max_kv);
-  a.splits = p.splits;
+  const Plan p = plan(D, heads, dt, a.T, a.n_seqs, a.hq, a.max_draft, a.max_kv);
+  a.want = p.want;
   a.row_groups = p.row_groups;
-  a.ws = static_cast<float*>(ws);
+  a.tile = kTileOf[p.form];
+  a.per_seq = int(a.T / a.n_seqs);
   a.blocks = int64_t(a.hq) * D / QK;
-  const int64_t grid = int64_t(heads) * p.splits * p.row_groups * a.n_seqs;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  a.ml = static_cast<float*>(ws);
+  a.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.ml);
+  const dim3 grid{unsigned(heads), unsigned(p.slots), unsigned(p.row_groups)};
   const bool f32 = dt == SKG_F32;
   hipError_t e;
   switch (kind) {
-    case KV_BF16: e = f32 ? tree_attn_bf16_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_bf16_bf16(a, D, p.rt, unsigned(grid), stream); break;
-    case KV_Q8_0: e = f32 ? tree_attn_q8_0_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_q8_0_bf16(a, D, p.rt, unsigned(grid), stream); break;
-    default: e = f32 ? tree_attn_q4_0_f32(a, D, p.rt, unsigned(grid), stream) : tree_attn_q4_0_bf16(a, D, p.rt, unsigned(grid), stream); break;
+    case KV_BF16: e = f32 ? tree_attn_bf16_f32(a, D, p.form, grid, stream) : tree_attn_bf16_bf16(a, D, p.form, grid, stream); break;
+    case KV_Q8_0: e = f32 ? tree_attn_q8_0_f32(a, D, p.form, grid, stream) : tree_attn_q8_0_bf16(a, D, p.form, grid, stream); break;
+    default: e = f32 ? tree_attn_q4_0_f32(a, D, p.form, grid, stream) : tree_attn_q4_0_bf16(a, D, p.form, grid, stream); break;
   }
-  if (e != hipSuccess || p.splits == 1) return e;
+  if (e != hipSuccess || !p.want) return e;
   const float unit = kind == KV_BF16 ? 1.f : kVScale;
-  return f32 ? join_dim<float>(a, D, unit, stream) : join_dim<__bf16>(a, D, unit, stream);
+  return f32 ? join_dim<float>(a, D, unit, p.wide, stream) : join_dim<__bf16>(a, D, unit, p.wide, stream);
 }
 
 }  // namespace skg

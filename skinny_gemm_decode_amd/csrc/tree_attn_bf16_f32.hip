@@ -3,6 +3,6 @@
 
 namespace skg {
 
-SKG_TREE_ATTN_DECL(tree_attn_bf16_f32) { return tree_attn_by_dim<float, KV_BF16>(a, D, rt, grid, stream); }
+SKG_TREE_ATTN_DECL(tree_attn_bf16_f32) { return tree_attn_by_dim<float, KV_BF16>(a, D, form, grid, stream); }
 
 }  // namespace skg

@@ -3,6 +3,6 @@
 
 namespace skg {
 
-SKG_TREE_ATTN_DECL(tree_attn_q4_0_bf16) { return tree_attn_by_dim<__bf16, KV_Q4_0>(a, D, rt, grid, stream); }
+SKG_TREE_ATTN_DECL(tree_attn_q4_0_bf16) { return tree_attn_by_dim<__bf16, KV_Q4_0>(a, D, form, grid, stream); }
 
 }  // namespace skg

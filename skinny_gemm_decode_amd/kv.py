@@ -252,10 +252,10 @@ def qkv_rope_store(cache: KvCache, q, k, v, slots, pos, inv_freq, gq=None, gk=No
     return qo
 
 
-def tree_attn_workspace(cache: KvCache, T: int, n_seqs: int, hq: int, max_draft: int, width: int,
+def tree_attn_workspace(cache: KvCache, dtype, T: int, n_seqs: int, hq: int, max_draft: int, width: int,
                         max_kv: int = 0) -> int:
     """Bytes of workspace that a tree_attn call of these counts needs (0: none)."""
-    return int(lib.skg_tree_attn_workspace(cache._ref, T, n_seqs, hq, max_draft, width, max_kv))
+    return int(lib.skg_tree_attn_workspace(cache._ref, _DTYPE[dtype], T, n_seqs, hq, max_draft, width, max_kv))
 
 
 def tree_attn(cache: KvCache, q, table, ctx, cu=None, mask=None, max_draft: int | None = None, max_kv: int = 0,
@@ -273,6 +273,9 @@ def tree_attn(cache: KvCache, q, table, ctx, cu=None, mask=None, max_draft: int 
     o: True or None to allocate [T, hq, D], a tensor to write into, False to
     skip it; oq: True or a tensor (uint8 [T, hq * D / 32, 36]) for the Q8_1
     blocks of o.  Returns o, or (o, oq) if oq was asked for.
+
+    workspace: tree_attn_workspace(...) bytes that no other call uses at the
+    time; None allocates it.
     """
     dev = _device(q, "q")
     dt = _dtype(q, "q")
@@ -304,13 +307,13 @@ def tree_attn(cache: KvCache, q, table, ctx, cu=None, mask=None, max_draft: int 
             oq = torch.empty((T, hq * D // 32, Q8_1_BLOCK_BYTES), dtype=torch.uint8, device=q.device)
             mine.append(oq)
         oqp = _flat(oq, "oq", nq, (torch.uint8,), dev)
-    size = int(lib.skg_tree_attn_workspace(cache._ref, T, n, hq, max_draft, width, max_kv))
+    size = int(lib.skg_tree_attn_workspace(cache._ref, dt, T, n, hq, max_draft, width, max_kv))
     wp = None
     if size:
         if workspace is None:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
             mine.append(workspace)
-        if workspace.get_device() != dev or not workspace.is_contiguous():
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on the current GPU")
         wp, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _on(stream, *mine)

@@ -143,6 +143,12 @@ CASES = [
     ([500], [3], 20, 1, 128, 1024),
     ([63, 64, 65], [1, 1, 1], 14, 2, 64, 128),
     ([1500], [1], 40, 8, 128, 256),
+    # many rows a cache head: the waves share rows (64, 128, 256 and past it), with splits and without
+    ([700], [16], 12, 3, 128, 16),
+    ([40, 900, 0], [3, 31, 2], 12, 3, 64, 32),
+    ([2000, 5], [64, 40], 16, 4, 128, 64),
+    ([100], [57], 10, 2, 256, 16),
+    ([300], [9], 16, 1, 64, 16),
 ]
 
 

@@ -148,6 +148,16 @@ def test_tree_attn_refusals(skg):
     for kw in (dict(q=ptr(0, 8)), dict(o=ptr(10, 4)), dict(oq=ptr(20, 2)), dict(cu=ptr(50, 2)), dict(mask=ptr(53, 4))):
         assert call(**kw) == skg.E_ALIGN, kw
     assert call(dt=BF16, oq=ptr(20)) == skg.E_UNSUPPORTED
+    # a long cache needs a workspace: absent, short, misaligned
+    size = skg.lib.skg_tree_attn_workspace(cache(skg, pages=1000), F32, 4, 2, 8, 2, 500, 0)
+    assert size > 0
+    long = dict(c=cache(skg, pages=1000, v=2000), width=500)
+    assert call(ws=ptr(60), wsb=size, **long) == skg.E_DEVICE
+    assert call(ws=ptr(60), wsb=size - 1, **long) == skg.E_INVALID_ARG
+    assert call(ws=None, wsb=size, **long) == skg.E_INVALID_ARG
+    assert call(ws=ptr(60, 128), wsb=size, **long) == skg.E_ALIGN
+    # the same cache with a small bound on its keys needs none
+    assert skg.lib.skg_tree_attn_workspace(cache(skg, pages=1000), F32, 4, 2, 8, 2, 500, 200) == 0
 
 
 def test_binding_refuses_host_tensors(skg):
