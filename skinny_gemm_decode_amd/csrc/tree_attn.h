@@ -29,6 +29,8 @@
 // be three bits below its bound).
 #pragma once
 
+#include <type_traits>
+
 #include "kv_common.h"
 #include "kernels.h"
 
@@ -212,8 +214,10 @@ __device__ inline void scaled_pair(float p0, float p1, uint32_t w0, uint32_t w1,
   const _Float16 h1 = static_cast<_Float16>(__builtin_fmaf(p1, float(s1), 0.f));
   t[0] = __builtin_bit_cast(uint32_t, f16x2{h0, h1});
   if constexpr (NT > 1) {
-    const _Float16 l0 = static_cast<_Float16>(__builtin_fmaf(p0, float(s0), -float(h0)));
-    const _Float16 l1 = static_cast<_Float16>(__builtin_fmaf(p1, float(s1), -float(h1)));
+    asm("" : "+v"(t[0]));  // read back from the pair, not computed once more
+    const f16x2 h = __builtin_bit_cast(f16x2, t[0]);
+    const _Float16 l0 = static_cast<_Float16>(__builtin_fmaf(p0, float(s0), -float(h.x)));
+    const _Float16 l1 = static_cast<_Float16>(__builtin_fmaf(p1, float(s1), -float(h.y)));
     t[1] = __builtin_bit_cast(uint32_t, f16x2{l0, l1});
   }
 }
@@ -276,10 +280,12 @@ struct AttnShape {
   static constexpr int kScales = !kF16 ? 0 : NB <= 4 ? 256 : 512;
   static constexpr int kSlot = 4 * kTile + 2 * kScales;
   static constexpr int kKOff = 0, kVOff = 2 * kTile, kSkOff = 4 * kTile, kSvOff = kSkOff + kScales;
-  // up to four slots where two workgroups (of four waves) still share a CU's 160 KB
+  // Workgroups of a CU: two of four waves, where they fit its 160 KB and 256
+  // registers a lane.  (A spilled register costs far more than its traffic
+  // here: waiting for its reload waits for every copy on its way.)
   static constexpr int kRings = ROWS ? 1 : W;
-  static constexpr int kFit = ((W == 4 ? 80 : 160) * 1024 - kQBytes) / (kRings * kSlot);
-  static constexpr int kPerCu = W == 4 && kFit >= 1 ? 2 : 1;
+  static constexpr int kPerCu = W == 4 && kRings * kSlot + kQBytes <= 80 * 1024 && D <= 128 && !(RT == 2 && kF16) ? 2 : 1;
+  static constexpr int kFit = (160 / kPerCu * 1024 - kQBytes - (kQLds ? 256 : 0)) / (kRings * kSlot);
   static constexpr int kSlots = kFit < 1 ? 1 : kFit > 4 ? 4 : kFit;
   // transfers of a wave: of K (or V) of a step, or of its part of both
   static constexpr int kCopies = kRow / 32 + kScales / 256;
@@ -330,25 +336,46 @@ __device__ inline void wait_ahead(int ahead, bool more) {
 }
 __device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Copies K (V = false) or V of the step's two 16-key tiles and their scales
-// into the slot at LDS address dst.  A page outside the cache is replaced by
-// page 0 (every key of it is masked).
+// A page outside the cache is replaced by page 0 (every key of it is masked).
+__device__ inline uint64_t pick(bool first, uint64_t a, uint64_t b) { return first ? a : b; }
 struct StepAt {
   uint64_t codes[2], scales[2];  // offsets of the tiles in the buffers of K and V
 };
+// The same for 32 steps at once, two lanes a step (its tiles).
+struct StepsAt {
+  uint64_t codes, scales;  // of the lane's tile
+  uint64_t there;          // bit: whether the lane's tile is in the cache
+};
+// page: the lane's; key: its tile's first key.
 template <int KIND, int D>
-__device__ inline StepAt step_at(const KvView& c, uint32_t head, int key, int32_t p0, int32_t p1) {
-  StepAt s;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int32_t page = t ? p1 : p0;
-    const uint64_t chunk = kv_chunk_at(c, kv_page_in(c, page) ? page : 0, head);
-    const uint32_t tok = uint32_t(key + 16 * t) & ((1u << c.shift) - 1);
-    s.codes[t] = chunk + kv_codes_at(KIND, D, tok);
-    s.scales[t] = chunk + kv_scales_at(KIND, D, c.shift, tok);
-  }
+__device__ inline StepsAt steps_at(const KvView& c, uint32_t head, int key, int32_t page) {
+  StepsAt s;
+  const bool in = kv_page_in(c, page);
+  s.there = __ballot(in);
+  const uint64_t chunk = kv_chunk_at(c, in ? page : 0, head);
+  const uint32_t tok = uint32_t(key) & ((1u << c.shift) - 1);
+  s.codes = chunk + kv_codes_at(KIND, D, tok);
+  s.scales = chunk + kv_scales_at(KIND, D, c.shift, tok);
   return s;
 }
+__device__ inline uint64_t lane64_of(uint64_t v, int lane) {
+  return uint64_t(uint32_t(lane_of(int(v), lane))) | uint64_t(uint32_t(lane_of(int(v >> 32), lane))) << 32;
+}
+// Step i's, i counted from a multiple of 32.
+template <bool SCALES>
+__device__ inline StepAt step_at(const StepsAt& s, int i) {
+  StepAt r{};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    r.codes[t] = lane64_of(s.codes, 2 * (i & 31) + t);
+    if constexpr (SCALES) r.scales[t] = lane64_of(s.scales, 2 * (i & 31) + t);
+  }
+  return r;
+}
+__device__ inline uint32_t there_of(const StepsAt& s, int i) { return uint32_t(s.there >> (2 * (i & 31))) & 3u; }
+
+// Copies K (V = false) or V of the step's two 16-key tiles and their scales
+// into the slot at LDS address dst.
 template <class S, int KIND, int D, bool V>
 __device__ inline void copy_step(const KvView& c, const StepAt& from, uint32_t dst) {
   const int lane = threadIdx.x & 63;
@@ -361,20 +388,20 @@ __device__ inline void copy_step(const KvView& c, const StepAt& from, uint32_t d
       for (int j = 0; j < S::kRow / 64; ++j) {
         const int row = j * (64 / S::kRC) + lane / S::kRC, unit = lane % S::kRC;
         const uint32_t off = V ? v_row(row) * S::kRow + 16 * unit : row * S::kRow + 16 * (unit ^ k_swizzle<S::kRC>(row));
-        dma16_sv(buf + from.codes[t], off, codes + t * S::kTile + 1024 * j);
+        dma16_sv_stream(buf + from.codes[t], off, codes + t * S::kTile + 1024 * j);
       }
   } else {  // both tiles in one transfer
     static_assert(S::kRow >= 64 || S::kRow == 32, "row");
     const int row = (lane & 31) / 2, unit = lane & 1;
-    const uint8_t* src = buf + (lane < 32 ? from.codes[0] : from.codes[1]);
-    dma16(src + (V ? v_row(row) : row) * S::kRow + 16 * unit, codes);
+    const uint8_t* src = buf + pick(lane < 32, from.codes[0], from.codes[1]);
+    dma16_stream(src + (V ? v_row(row) : row) * S::kRow + 16 * unit, codes);
   }
   if constexpr (S::kF16) {
     // 16 NB words over both tiles (NB = 2: the upper lanes repeat the lower)
 #pragma unroll
     for (int j = 0; j < S::kScales / 256; ++j) {
       const int w = (64 * j + lane) % (16 * S::NB), t = w / (8 * S::NB);
-      dma4(buf + (t ? from.scales[1] : from.scales[0]) + 4 * (w - t * 8 * S::NB), dst + (V ? S::kSvOff : S::kSkOff) + 256 * j);
+      dma4(buf + pick(t != 0, from.scales[1], from.scales[0]) + 4 * (w - t * 8 * S::NB), dst + (V ? S::kSvOff : S::kSkOff) + 256 * j);
     }
   }
 }
@@ -398,7 +425,7 @@ __device__ inline void copy_part(const KvView& c, const StepAt& from, uint32_t d
       dma16_sv(buf + (t ? from.codes[1] : from.codes[0]), off, dst + (v ? S::kVOff : S::kKOff) + t * S::kTile + 1024 * i);
     } else {
       const int row = (lane & 31) / 2, unit = lane & 1;
-      const uint8_t* src = buf + (lane < 32 ? from.codes[0] : from.codes[1]);
+      const uint8_t* src = buf + pick(lane < 32, from.codes[0], from.codes[1]);
       dma16(src + (v ? v_row(row) : row) * S::kRow + 16 * unit, dst + (v ? S::kVOff : S::kKOff));
     }
   }
@@ -408,7 +435,7 @@ __device__ inline void copy_part(const KvView& c, const StepAt& from, uint32_t d
 #pragma unroll
     for (int j = 0; j < S::kScales / 256; ++j) {
       const int w = (64 * j + lane) % (16 * S::NB), t = w / (8 * S::NB);
-      dma4(buf + (t ? from.scales[1] : from.scales[0]) + 4 * (w - t * 8 * S::NB), dst + (v ? S::kSvOff : S::kSkOff) + 256 * j);
+      dma4(buf + pick(t != 0, from.scales[1], from.scales[0]) + 4 * (w - t * 8 * S::NB), dst + (v ? S::kSvOff : S::kSkOff) + 256 * j);
     }
   }
 }
@@ -442,6 +469,7 @@ struct StepRegs {
   uint32_t v[8][S::VW];   // keys 4g + i (tile 0), 4g + i - 4 (tile 1), column c
   uint32_t sk[2][S::SW];  // scales of keys 4g .. 4g + 3 of each tile
   uint32_t sv[2][S::SW];
+  uint32_t all[2];        // the step's scales of V, spread over the lanes
   int key;                // first key
   bool there[2];          // whether a tile's page is in the cache
 };
@@ -478,6 +506,8 @@ __device__ inline void read_v(StepRegs<S>& r, const uint8_t* slot) {
     }
     if constexpr (S::kF16) load_words<S::SW>(slot + S::kSvOff + (16 * t + 4 * g) * 2 * S::NB, r.sv[t]);
   }
+#pragma unroll
+  for (int j = 0; j < S::kScales / 256; ++j) r.all[j] = reinterpret_cast<const uint32_t*>(slot + S::kSvOff)[64 * j + lane];
 }
 
 // K operand of block b of tile t: elements 8g .. 8g + 7 of the block (for q4_0
@@ -612,8 +642,7 @@ __device__ inline void do_scores(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, floa
 // The softmax's step and the sums with V.  EDGE: keys that are not there, or
 // that not every row sees.
 template <class S, int KIND, int D, int NT, int RT, bool EDGE>
-__device__ inline void do_values(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, float (&s)[RT][8], int ctx, int keys,
-                                 const uint8_t* slot) {
+__device__ inline void do_values(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, float (&s)[RT][8], int ctx, int keys) {
   constexpr int NB = S::NB;
   const int lane = threadIdx.x & 63, g = lane >> 4;
   uint32_t seen[RT];  // bit i: whether the row sees the lane's key i
@@ -647,10 +676,9 @@ __device__ inline void do_values(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, floa
         }
       }
     } else {  // every row sees all: the scales spread over the lanes
-      const uint32_t* sv = reinterpret_cast<const uint32_t*>(slot + S::kSvOff);
 #pragma unroll
       for (int j = 0; j < S::kScales / 256; ++j) {
-        const uint32_t x = sv[64 * j + lane] & 0x7FFF7FFFu;
+        const uint32_t x = r.all[j] & 0x7FFF7FFFu;
         big = max(big, max(x & 0xFFFFu, x >> 16));
       }
     }
@@ -992,25 +1020,20 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
     row_of(a, row, is, i, h);
     w.mask[rt] = !is ? 0 : a.mask ? a.mask[sp.t0 + i] : ~uint64_t(0) >> (63 - i);
   }
-  // pages of the wave's next 32 steps, two tiles each, over its lanes
+  // where the wave's next 32 steps lie, two tiles each, over its lanes
   const int32_t* table = a.table + int64_t(unit.seq) * a.width;
   auto key_of = [&](int i) SKG_INL { return (unit.begin + wave + i * kWaves) * kStep; };
-  auto pages_of = [&](int i0) SKG_INL -> int32_t {
+  auto where_from = [&](int i0) SKG_INL {
     const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
-    return i < n && key < sp.keys ? table[key >> a.cache.shift] : -1;
+    return steps_at<KIND, D>(a.cache, head, key, i < n && key < sp.keys ? table[key >> a.cache.shift] : -1);
   };
-  int32_t pages = pages_of(0);
+  StepsAt where = where_from(0);
   uint8_t* ring = lds + wave * (S::kSlots * S::kSlot);
   const uint32_t ring_at = lds_addr(ring);
-  auto page = [&](int i, int t) SKG_INL { return lane_of(pages, 2 * (i & 31) + t); };
-  auto at_of = [&](int i) SKG_INL { return step_at<KIND, D>(a.cache, head, key_of(i), page(i, 0), page(i, 1)); };
-  auto there_of = [&](int i) SKG_INL -> uint32_t {
-    return uint32_t(kv_page_in(a.cache, page(i, 0))) | uint32_t(kv_page_in(a.cache, page(i, 1))) << 1;
-  };
-  uint32_t flags = 0;  // the copied steps' pages in the cache, two bits each, oldest first
+  uint32_t flags = 0;  // the copied steps' tiles in the cache, two bits each, oldest first
   auto copy_both = [&](int i) SKG_INL {
-    flags |= there_of(i) << (2 * i);
-    const StepAt from = at_of(i);
+    flags |= there_of(where, i) << (2 * i);
+    const StepAt from = step_at<S::kF16>(where, i);
     copy_step<S, KIND, D, false>(a.cache, from, ring_at + i * S::kSlot);
     copy_step<S, KIND, D, true>(a.cache, from, ring_at + i * S::kSlot);
   };
@@ -1049,10 +1072,10 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
   w.be = -40;
 
   int slot = 0;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
+  auto step = [&](int i, auto edge) SKG_INL {
     const int ahead = n - 1 - i < S::kSlots - 1 ? n - 1 - i : S::kSlots - 1;  // later steps on their way
-    const bool more = i + S::kSlots < n;
+    const int later = i + S::kSlots;
+    const bool more = later < n;
     uint8_t* at = ring + slot * S::kSlot;
     StepRegs<S> r;
     r.key = key_of(i);
@@ -1063,26 +1086,29 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
     StepAt next;
     wait_ahead<S::kCopies, S::kSlots, true>(ahead, false);
     read_k<S, KIND>(r, at);
-    do_scores<S, KIND, D, NT, RT>(w, r, s);
     if (more) {
-      if (((i + S::kSlots) & 31) == 0) pages = pages_of(i + S::kSlots);
-      flags |= there_of(i + S::kSlots) << (2 * (S::kSlots - 1));
-      next = at_of(i + S::kSlots);
+      if ((later & 31) == 0) where = where_from(later);
+      flags |= there_of(where, later) << (2 * (S::kSlots - 1));
+      next = step_at<S::kF16>(where, later);
       wait_lds();
       copy_step<S, KIND, D, false>(a.cache, next, ring_at + slot * S::kSlot);
     }
+    do_scores<S, KIND, D, NT, RT>(w, r, s);
     wait_ahead<S::kCopies, S::kSlots, false>(ahead, more);
     read_v<S, KIND>(r, at);
-    if (r.key + kStep <= sp.ctx && r.there[0] && r.there[1])
-      do_values<S, KIND, D, NT, RT, false>(w, r, s, sp.ctx, sp.keys, at);
-    else
-      do_values<S, KIND, D, NT, RT, true>(w, r, s, sp.ctx, sp.keys, at);
     if (more) {
       wait_lds();
       copy_step<S, KIND, D, true>(a.cache, next, ring_at + slot * S::kSlot);
     }
+    do_values<S, KIND, D, NT, RT, edge()>(w, r, s, sp.ctx, sp.keys);
     slot = slot + 1 == S::kSlots ? 0 : slot + 1;
-  }
+  };
+  // steps that every row sees whole, then (from the first that is not) the rest
+  int i = 0;
+#pragma unroll 1
+  for (; i < n && (flags & 3) == 3 && key_of(i) + kStep <= sp.ctx; ++i) step(i, std::false_type{});
+#pragma unroll 1
+  for (; i < n; ++i) step(i, std::true_type{});
 
   // Join the waves: lane t of the sixteen of row jr sums elements 32 k + 2 t and
   // the next.
@@ -1146,7 +1172,7 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
 // them.  One barrier a step: past it the step's copies (each wave waits for its
 // own before it) are there and the slot of the step before is free.
 template <class T, int KIND, int D, int NT, int RT, int W>
-__global__ __launch_bounds__(64 * W, (W == 8 || D <= 128 ? 2 : 1)) void tree_attn_rows_kernel(TreeArgs a) {
+__global__ __launch_bounds__(64 * W, (W == 8 ? 2 : AttnShape<KIND, D, NT, RT, W, true>::kPerCu)) void tree_attn_rows_kernel(TreeArgs a) {
   using S = AttnShape<KIND, D, NT, RT, W, true>;
   constexpr int C = S::C, NB = S::NB, B = C / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
@@ -1175,18 +1201,16 @@ __global__ __launch_bounds__(64 * W, (W == 8 || D <= 128 ? 2 : 1)) void tree_att
   }
   const int32_t* table = a.table + int64_t(unit.seq) * a.width;
   auto key_of = [&](int i) SKG_INL { return (unit.begin + i) * kStep; };
-  auto pages_of = [&](int i0) SKG_INL -> int32_t {
+  auto where_from = [&](int i0) SKG_INL {
     const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
-    return i < n && key < sp.keys ? table[key >> a.cache.shift] : -1;
+    return steps_at<KIND, D>(a.cache, head, key, i < n && key < sp.keys ? table[key >> a.cache.shift] : -1);
   };
-  int32_t pages = pages_of(0);
+  StepsAt where = where_from(0);
   const uint32_t ring_at = lds_addr(lds);
-  auto page = [&](int i, int t) SKG_INL { return lane_of(pages, 2 * (i & 31) + t); };
-  uint32_t flags = 0;  // the copied steps' pages in the cache, two bits each, oldest first
+  uint32_t flags = 0;  // the copied steps' tiles in the cache, two bits each, oldest first
   auto copy = [&](int i, int slot, int at) SKG_INL {
-    const int32_t p0 = page(i, 0), p1 = page(i, 1);
-    flags |= (uint32_t(kv_page_in(a.cache, p0)) | uint32_t(kv_page_in(a.cache, p1)) << 1) << (2 * at);
-    copy_part<S, KIND, D, W>(a.cache, step_at<KIND, D>(a.cache, head, key_of(i), p0, p1), ring_at + slot * S::kSlot, wave);
+    flags |= there_of(where, i) << (2 * at);
+    copy_part<S, KIND, D, W>(a.cache, step_at<S::kF16>(where, i), ring_at + slot * S::kSlot, wave);
   };
 #pragma unroll 1
   for (int i = 0; i < S::kSlots - 1 && i < n; ++i) copy(i, i, i);
@@ -1206,35 +1230,36 @@ __global__ __launch_bounds__(64 * W, (W == 8 || D <= 128 ? 2 : 1)) void tree_att
   if constexpr (S::kSubnormal) fill_zero<S, KIND, NB, NT>(w);
 
   int slot = 0;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
+  auto step = [&](int i, auto edge) SKG_INL {
     wait_parts<S::kPart, S::kSlots - 2>(n - 1 - i);
     wait_lds();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const int next = i + S::kSlots - 1;
-    if (next < n) {
-      if ((next & 31) == 0) pages = pages_of(next);
-      copy(next, slot == 0 ? S::kSlots - 1 : slot - 1, S::kSlots - 1);
-    }
     const uint8_t* at = lds + slot * S::kSlot;
     StepRegs<S> r;
     r.key = key_of(i);
     r.there[0] = flags & 1;
     r.there[1] = flags & 2;
     flags >>= 2;
+    const int later = i + S::kSlots - 1;
+    if (later < n) {
+      if ((later & 31) == 0) where = where_from(later);
+      copy(later, slot == 0 ? S::kSlots - 1 : slot - 1, S::kSlots - 2);
+    }
     if (first < rows) {  // a wave without rows copies only
       float s[RT][8];
       read_k<S, KIND>(r, at);
       do_scores<S, KIND, D, NT, RT>(w, r, s);
       read_v<S, KIND>(r, at);
-      if (r.key + kStep <= sp.ctx && r.there[0] && r.there[1])
-        do_values<S, KIND, D, NT, RT, false>(w, r, s, sp.ctx, sp.keys, at);
-      else
-        do_values<S, KIND, D, NT, RT, true>(w, r, s, sp.ctx, sp.keys, at);
+      do_values<S, KIND, D, NT, RT, edge()>(w, r, s, sp.ctx, sp.keys);
     }
     slot = slot + 1 == S::kSlots ? 0 : slot + 1;
-  }
+  };
+  int i = 0;
+#pragma unroll 1
+  for (; i < n && (flags & 3) == 3 && key_of(i) + kStep <= sp.ctx; ++i) step(i, std::false_type{});
+#pragma unroll 1
+  for (; i < n; ++i) step(i, std::true_type{});
 
   // each wave's rows through its part of LDS, four rows of 16 lanes at a time
   __syncthreads();
