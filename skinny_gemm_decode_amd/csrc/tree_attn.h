@@ -290,7 +290,7 @@ struct AttnShape {
   // transfers of a wave: of K (or V) of a step, or of its part of both
   static constexpr int kCopies = kRow / 32 + kScales / 256;
   static constexpr int kPart = (2 * kRow / 32 + W - 1) / W + kScales / 256;
-  static_assert(ROWS ? kPart * kSlots <= 63 && kSlots >= 2 : kCopies * (2 * kSlots + 1) <= 63, "vmcnt");
+  static_assert(ROWS ? kPart * kSlots <= 63 && kSlots >= 2 : 2 * kCopies * kSlots <= 63, "vmcnt");
 
   // LDS: the ring and q; after the last step the waves' sums, M and l
   static constexpr int C = D < 128 ? D : 128;  // elements joined at a time
@@ -322,16 +322,14 @@ template <int N>
 __device__ inline void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-// Waits for a step's K (or V) while `ahead` later steps, and for V the K of
-// one more, are on their way.  C copies for each of K and V.
-template <int C, int SLOTS, bool K>
-__device__ inline void wait_ahead(int ahead, bool more) {
-  if (more) {
-    wait_copies<2 * C * (SLOTS - 1) + C>();
-  } else if (ahead == SLOTS - 1) {
-    wait_copies<2 * C * (SLOTS - 1) + (K ? C : 0)>();
+// Waits for a step while `ahead` later ones are on their way: C copies for each
+// of K and V.
+template <int C, int SLOTS>
+__device__ inline void wait_ahead(int ahead) {
+  if (ahead == SLOTS - 1) {
+    wait_copies<2 * C * (SLOTS - 1)>();
   } else if constexpr (SLOTS > 1) {
-    wait_ahead<C, SLOTS - 1, K>(ahead, false);
+    wait_ahead<C, SLOTS - 1>(ahead);
   }
 }
 __device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -1071,6 +1069,11 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
   }
   w.be = -40;
 
+  // A SIMD serves its oldest wave first, so of two workgroups of a CU the first
+  // ran ahead and left the other alone, at one wave a SIMD, for the last third.
+  // The further a wave is, the lower its priority.
+  __builtin_amdgcn_s_setprio(3);
+  const int n1 = n / 4 - 1, n2 = n / 2 - 1, n3 = 3 * n / 4 - 1;
   int slot = 0;
   auto step = [&](int i, auto edge) SKG_INL {
     const int ahead = n - 1 - i < S::kSlots - 1 ? n - 1 - i : S::kSlots - 1;  // later steps on their way
@@ -1083,25 +1086,23 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
     r.there[1] = flags & 2;
     flags >>= 2;
     float s[RT][8];
-    StepAt next;
-    wait_ahead<S::kCopies, S::kSlots, true>(ahead, false);
+    wait_ahead<S::kCopies, S::kSlots>(ahead);
     read_k<S, KIND>(r, at);
+    read_v<S, KIND>(r, at);
+    do_scores<S, KIND, D, NT, RT>(w, r, s);
     if (more) {
       if ((later & 31) == 0) where = where_from(later);
       flags |= there_of(where, later) << (2 * (S::kSlots - 1));
-      next = step_at<S::kF16>(where, later);
-      wait_lds();
+      const StepAt next = step_at<S::kF16>(where, later);
+      wait_lds();  // its slot is this step's, read by now
       copy_step<S, KIND, D, false>(a.cache, next, ring_at + slot * S::kSlot);
-    }
-    do_scores<S, KIND, D, NT, RT>(w, r, s);
-    wait_ahead<S::kCopies, S::kSlots, false>(ahead, more);
-    read_v<S, KIND>(r, at);
-    if (more) {
-      wait_lds();
       copy_step<S, KIND, D, true>(a.cache, next, ring_at + slot * S::kSlot);
     }
     do_values<S, KIND, D, NT, RT, edge()>(w, r, s, sp.ctx, sp.keys);
     slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+    if (i == n1) __builtin_amdgcn_s_setprio(2);
+    if (i == n2) __builtin_amdgcn_s_setprio(1);
+    if (i == n3) __builtin_amdgcn_s_setprio(0);
   };
   // steps that every row sees whole, then (from the first that is not) the rest
   int i = 0;
