@@ -15,10 +15,10 @@
 // no exchange (lanes past the rotated part hold two adjacent units).  The sum
 // of squares meets over the row's 4..32 lanes.
 //
-// Cache rows.  The encoder and decoder give a lane the element pair
-// (2c, 2c + 1) of blocks 2 bp and 2 bp + 1, c = lane & 15: the loads of a
-// 16-lane row are 128 contiguous bytes of binary32, a block's maximum is four
-// DPP steps, and the lane's four codes are adjacent in the cache row.
+// Cache rows.  The encoder gives a lane the element pair (2c, 2c + 1) of blocks
+// 2 bp and 2 bp + 1, c = lane & 15: the loads of a 16-lane row are 128
+// contiguous bytes of binary32, a block's maximum is four DPP steps, and the
+// lane's four codes are adjacent in the cache row.
 #include "kv_common.h"
 #include "kernels.h"
 
@@ -27,6 +27,7 @@ namespace skg {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kManyGroups = 1024;  // four workgroups a CU
 
 template <int CTRL>
 __device__ inline int dpp_u(int v) {
@@ -169,7 +170,12 @@ __device__ inline void fill_angles(const RopeArgs& r, int64_t tok, f32x2* cs) {
   if (t < r.rot / 2) cs[t] = cos_sin(r.pos[tok], r.inv_freq[t]);
 }
 
-// P rows per thread, all loaded before the first is used.
+// P rows per thread, all loaded before the first is used.  Two of them where
+// there are workgroups enough all the same: 32 + 8 heads of 128 bf16 elements
+// of 8191 tokens 43.7 us with one, 33.6 with two or four, 31.7 with two and
+// stores past the caches (168 MB: 5.3 TB/s); 64 heads of 512 binary32 tokens
+// 7.3, 7.4, 7.8 and 6.4 us.  A small call keeps one, for its latency (one token's
+// 64 heads 2.1 us, with two 2.5), and its rows in the caches for their reader.
 template <class T, int D, int P>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(Rows q, Rows k, Rows qo, Rows ko, int hq, int hk,
                                                                 int chunks, RopeArgs r) {
@@ -205,8 +211,13 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(Rows q, Rows k, 
       norm_rope<T, D>(a, b, l, ua, ub, r, isq ? r.gq : r.gk, cs);
       u32x4* dst = reinterpret_cast<u32x4*>((isq ? qo.p : ko.p) + tok * (isq ? qo.ld : ko.ld)) +
                    (isq ? row : row - hq) * S::kUnits;
-      dst[ua] = Elem<T>::pack(a);
-      dst[ub] = Elem<T>::pack(b);
+      if constexpr (P > 1) {
+        __builtin_nontemporal_store(Elem<T>::pack(a), dst + ua);
+        __builtin_nontemporal_store(Elem<T>::pack(b), dst + ub);
+      } else {
+        dst[ua] = Elem<T>::pack(a);
+        dst[ub] = Elem<T>::pack(b);
+      }
     }
   }
 }
@@ -279,97 +290,100 @@ __device__ inline void put_row(uint8_t* chunk, uint32_t shift, uint32_t tok, int
   }
 }
 
-template <int KIND, int D>
-__device__ inline void get_row(const uint8_t* chunk, uint32_t shift, uint32_t tok, int c, int bp, f32x2& x,
-                               f32x2& y) {
+// The decoder's lane (j, bp) takes a 16-byte unit of the output in each of
+// blocks 2 bp and 2 bp + 1: elements V j .. V j + V - 1, from V / 2 columns.
+template <class T, int D>
+struct UnitShape {
+  static constexpr int kBlock = 32 / Elem<T>::kVec;  // lanes of a block
+  static constexpr int kLanes = kBlock * (D / 64);   // of a row
+  static constexpr int kRows = kThreads / kLanes;    // rows of a pass
+};
+template <class T, int KIND, int D>
+__device__ inline void get_units(const uint8_t* chunk, uint32_t shift, uint32_t tok, int j, int bp,
+                                 float (&x)[Elem<T>::kVec], float (&y)[Elem<T>::kVec]) {
+  constexpr int V = Elem<T>::kVec;
   const uint8_t* row = chunk + kv_codes_at(KIND, D, tok);
   if constexpr (KIND == KV_BF16) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + 32 * bp + c;
-    x = f32x2{bf16_lo(w[0]), bf16_hi(w[0])};
-    y = f32x2{bf16_lo(w[16]), bf16_hi(w[16])};
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + 32 * bp + V / 2 * j;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+      y[2 * i] = bf16_lo(w[16 + i]);
+      y[2 * i + 1] = bf16_hi(w[16 + i]);
+    }
   } else {
     constexpr int NB = D / 32;
     const uint32_t s = *reinterpret_cast<const uint32_t*>(chunk + kv_scales_at(KIND, D, shift, tok) + 4 * bp);
     const float d0 = h2f(s & 0xFFFFu), d1 = h2f(s >> 16);
-    if constexpr (KIND == KV_Q8_0) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 2 * NB * c + 4 * bp);
-      x = f32x2{d0 * (cvt_ubyte<0>(w) - 128.f), d0 * (cvt_ubyte<1>(w) - 128.f)};
-      y = f32x2{d1 * (cvt_ubyte<2>(w) - 128.f), d1 * (cvt_ubyte<3>(w) - 128.f)};
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(row + NB * c + 2 * bp);
-      x = f32x2{d0 * (float(w & 15u) - 8.f), d0 * (float((w >> 4) & 15u) - 8.f)};
-      y = f32x2{d1 * (float((w >> 8) & 15u) - 8.f), d1 * (float(w >> 12) - 8.f)};
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const int c = V / 2 * j + i;
+      if constexpr (KIND == KV_Q8_0) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 2 * NB * c + 4 * bp);
+        x[2 * i] = d0 * (cvt_ubyte<0>(w) - 128.f);
+        x[2 * i + 1] = d0 * (cvt_ubyte<1>(w) - 128.f);
+        y[2 * i] = d1 * (cvt_ubyte<2>(w) - 128.f);
+        y[2 * i + 1] = d1 * (cvt_ubyte<3>(w) - 128.f);
+      } else {
+        const uint32_t w = *reinterpret_cast<const uint16_t*>(row + NB * c + 2 * bp);
+        x[2 * i] = d0 * (float(w & 15u) - 8.f);
+        x[2 * i + 1] = d0 * (float((w >> 4) & 15u) - 8.f);
+        y[2 * i] = d1 * (float((w >> 8) & 15u) - 8.f);
+        y[2 * i + 1] = d1 * (float(w >> 12) - 8.f);
+      }
     }
   }
 }
 
-// Keys (blockIdx.y == 0) or values of P rows per thread into the cache.
-template <class T, int KIND, int D, int P>
+// Keys (blockIdx.y == 0) or values into the cache.
+template <class T, int KIND, int D>
 __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvView cache, Rows k, Rows v, const int64_t* slots,
                                                             int64_t rows) {
   constexpr int L = PairShape<D>::kLanes;
   const Rows in = blockIdx.y ? v : k;
   uint8_t* buf = blockIdx.y ? cache.v : cache.k;
   const int lane = threadIdx.x % L, c = lane & 15, bp = lane >> 4;
-  const int64_t first = int64_t(blockIdx.x) * PairShape<D>::kRows * P + threadIdx.x / L;
-  f32x2 x[P], y[P];
-  int64_t slot[P];
-  uint32_t head[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int64_t r = first + p * PairShape<D>::kRows;
-    slot[p] = -1;
-    x[p] = y[p] = f32x2{0.f, 0.f};
-    head[p] = 0;
-    if (r < rows) {
-      const uint32_t tok = uint32_t(r / cache.heads);
-      head[p] = uint32_t(r - int64_t(tok) * cache.heads);
-      const uint8_t* src = in.p + tok * in.ld + (int64_t(head[p]) * D + 64 * bp + 2 * c) * int(sizeof(T));
-      x[p] = Elem<T>::pair(src);
-      y[p] = Elem<T>::pair(src + 32 * sizeof(T));
-      slot[p] = slots[tok];
-    }
+  const int64_t r = int64_t(blockIdx.x) * PairShape<D>::kRows + threadIdx.x / L;
+  f32x2 x{0.f, 0.f}, y{0.f, 0.f};
+  int64_t slot = -1;
+  uint32_t head = 0;
+  if (r < rows) {
+    const uint32_t tok = uint32_t(r / cache.heads);
+    head = uint32_t(r - int64_t(tok) * cache.heads);
+    const uint8_t* src = in.p + tok * in.ld + (int64_t(head) * D + 64 * bp + 2 * c) * int(sizeof(T));
+    x = Elem<T>::pair(src);
+    y = Elem<T>::pair(src + 32 * sizeof(T));
+    slot = slots[tok];
   }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const bool in_cache = kv_slot_in(cache, slot[p]);
-    const int64_t s = in_cache ? slot[p] : 0;
-    put_row<KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head[p]), cache.shift,
-                     uint32_t(s & ((int64_t(1) << cache.shift) - 1)), c, bp, x[p], y[p], in_cache);
-  }
+  const bool in_cache = kv_slot_in(cache, slot);
+  const int64_t s = in_cache ? slot : 0;
+  put_row<KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
+                   uint32_t(s & ((int64_t(1) << cache.shift) - 1)), c, bp, x, y, in_cache);
 }
 
-template <class T, int KIND, int D, int P>
+// The cache's keys (blockIdx.y == 0) or values as rows.  Bound by the bytes
+// written: 16383 rows of 4 heads of 256 from q8_0 to bf16 (103 MB) with the
+// store of 1000 of them 24.0 us, where the encoder's lanes (an element pair of
+// two blocks, 4-byte stores) took 34.2 and stores past the caches 27.
+template <class T, int KIND, int D>
 __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvView cache, Rows k, Rows v, const int64_t* slots,
                                                            int64_t rows) {
-  constexpr int L = PairShape<D>::kLanes;
+  using S = UnitShape<T, D>;
   const Rows out = blockIdx.y ? v : k;
   const uint8_t* buf = blockIdx.y ? cache.v : cache.k;
-  const int lane = threadIdx.x % L, c = lane & 15, bp = lane >> 4;
-  const int64_t first = int64_t(blockIdx.x) * PairShape<D>::kRows * P + threadIdx.x / L;
-  f32x2 x[P], y[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int64_t r = first + p * PairShape<D>::kRows;
-    x[p] = y[p] = f32x2{0.f, 0.f};
-    if (r < rows) {
-      const uint32_t tok = uint32_t(r / cache.heads), head = uint32_t(r - int64_t(tok) * cache.heads);
-      const int64_t s = slots[tok];
-      if (kv_slot_in(cache, s))
-        get_row<KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
-                         uint32_t(s & ((int64_t(1) << cache.shift) - 1)), c, bp, x[p], y[p]);
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int64_t r = first + p * PairShape<D>::kRows;
-    if (r < rows) {
-      const uint32_t tok = uint32_t(r / cache.heads), head = uint32_t(r - int64_t(tok) * cache.heads);
-      uint8_t* dst = out.p + tok * out.ld + (int64_t(head) * D + 64 * bp + 2 * c) * int(sizeof(T));
-      Elem<T>::put_pair(dst, x[p].x, x[p].y);
-      Elem<T>::put_pair(dst + 32 * sizeof(T), y[p].x, y[p].y);
-    }
-  }
+  const int lane = threadIdx.x % S::kLanes, j = lane % S::kBlock, bp = lane / S::kBlock;
+  const int64_t r = int64_t(blockIdx.x) * S::kRows + threadIdx.x / S::kLanes;
+  if (r >= rows) return;
+  float x[Elem<T>::kVec] = {}, y[Elem<T>::kVec] = {};
+  const uint32_t tok = uint32_t(r / cache.heads), head = uint32_t(r - int64_t(tok) * cache.heads);
+  const int64_t s = slots[tok];
+  if (kv_slot_in(cache, s))
+    get_units<T, KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
+                          uint32_t(s & ((int64_t(1) << cache.shift) - 1)), j, bp, x, y);
+  u32x4* dst = reinterpret_cast<u32x4*>(out.p + tok * out.ld + (int64_t(head) * D + 64 * bp) * int(sizeof(T))) + j;
+  dst[0] = Elem<T>::pack(x);
+  dst[S::kBlock] = Elem<T>::pack(y);
 }
 
 // Rotation and store in one launch.  Workgroups 0 .. rope_chunks - 1 of a
@@ -482,12 +496,16 @@ hipError_t launch_qk_norm_rope(skg_dtype dt, int64_t T, int hq, int hk, int D, c
     return by_dim(D, [&](auto d) {
       using E = decltype(t);
       constexpr int N = RowShape<E, d()>::kRows;
-      const int64_t chunks = (hq + hk + N - 1) / N;
-      if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
-      hipLaunchKernelGGL((qk_norm_rope_kernel<E, d(), 1>), dim3(unsigned(T * chunks)), dim3(kThreads), 0, stream,
-                         rows_of(q, ldq, dt), rows_of(k, ldk, dt), rows_of(qo, ldqo, dt), rows_of(ko, ldko, dt), hq,
-                         hk, int(chunks), rope_args(rope));
-      return hipGetLastError();
+      auto launch = [&](auto kernel, int rows) {  // rows of a workgroup
+        const int64_t chunks = (hq + hk + rows - 1) / rows;
+        if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(kernel, dim3(unsigned(T * chunks)), dim3(kThreads), 0, stream, rows_of(q, ldq, dt),
+                           rows_of(k, ldk, dt), rows_of(qo, ldqo, dt), rows_of(ko, ldko, dt), hq, hk, int(chunks),
+                           rope_args(rope));
+        return hipGetLastError();
+      };
+      if (T * ((hq + hk + N - 1) / N) >= kManyGroups) return launch(qk_norm_rope_kernel<E, d(), 2>, 2 * N);
+      return launch(qk_norm_rope_kernel<E, d(), 1>, N);
     });
   });
 }
@@ -499,7 +517,7 @@ hipError_t launch_kv_store(const KvView& c, int kind, int D, skg_dtype dt, int64
       return by_kind(kind, [&](auto kd) {
         const int64_t rows = T * c.heads, grid = (rows + PairShape<d()>::kRows - 1) / PairShape<d()>::kRows;
         if (grid > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((kv_store_kernel<decltype(t), kd(), d(), 1>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
+        hipLaunchKernelGGL((kv_store_kernel<decltype(t), kd(), d()>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
                            stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, rows);
         return hipGetLastError();
       });
@@ -512,9 +530,9 @@ hipError_t launch_kv_load(const KvView& c, int kind, int D, skg_dtype dt, int64_
   return by_type(dt, [&](auto t) {
     return by_dim(D, [&](auto d) {
       return by_kind(kind, [&](auto kd) {
-        const int64_t rows = T * c.heads, grid = (rows + PairShape<d()>::kRows - 1) / PairShape<d()>::kRows;
+        const int64_t rows = T * c.heads, grid = (rows + UnitShape<decltype(t), d()>::kRows - 1) / UnitShape<decltype(t), d()>::kRows;
         if (grid > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((kv_load_kernel<decltype(t), kd(), d(), 1>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
+        hipLaunchKernelGGL((kv_load_kernel<decltype(t), kd(), d()>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
                            stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, rows);
         return hipGetLastError();
       });

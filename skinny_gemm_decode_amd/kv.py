@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from . import Q8_1_BLOCK_BYTES, _stream, check, lib
+from . import OK, Q8_1_BLOCK_BYTES, _stream, check, lib
 
 # skg_kv_fmt
 KV_BF16, KV_Q8_0, KV_Q4_0 = range(3)
@@ -81,6 +81,17 @@ def kv_cache(fmt: int, heads: int, head_dim: int, page_size: int, pages: int, de
     return KvCache(fmt, heads, head_dim, page_size, k, v)
 
 
+# A decode step's small calls cost more here than on the GPU (a launch is 2 to
+# 4 us of the host's time, torch.cuda.current_stream() alone 2.8), so what every
+# call does is kept short: the stream's handle without a Stream object around
+# it, and no checks of tensors that are made here.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_stream(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def _device(t, what: str) -> int:
     """The current device, which has to be t's."""
     if not t.is_cuda:
@@ -98,18 +109,19 @@ def _dtype(t, what: str) -> int:
     return dt
 
 
-def _rows(t, what: str, T: int, heads: int, D: int, dtype, dev: int):
+def _rows(t, what: str, shape, dtype, dev: int):
     """Pointer and token stride (elements) of rows [T, heads, D]."""
-    if t.dim() != 3 or t.shape != (T, heads, D):
-        raise ValueError(f"{what} must be [{T}, {heads}, {D}] (got {list(t.shape)})")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)} (got {list(t.shape)})")
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} (got {t.dtype})")
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current GPU")
-    s = t.stride()
-    if s[2] != 1 or (s[1] != D and heads > 1):
-        raise ValueError(f"the heads of {what} must be adjacent (strides {list(s)})")
-    return t.data_ptr(), s[0] if T > 1 else heads * D
+    T, heads, D = shape
+    ld, head, one = t.stride()
+    if one != 1 or (head != D and heads > 1):
+        raise ValueError(f"the heads of {what} must be adjacent (strides {list(t.stride())})")
+    return t.data_ptr(), ld if T > 1 else heads * D
 
 
 def _flat(t, what: str, n: int, dtypes, dev: int) -> int:
@@ -126,11 +138,9 @@ def _flat(t, what: str, n: int, dtypes, dev: int) -> int:
 _I32, _I64, _F32, _MASK = (torch.int32,), (torch.int64,), (torch.float32,), (torch.int64, torch.uint64)
 
 
-def _on(stream, *tensors):
+def _on(stream, tensors):
     """Tells the allocator of tensors made here that `stream`, not the current
     stream, uses them."""
-    if stream is None or not tensors:
-        return
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
@@ -176,20 +186,29 @@ def qk_norm_rope(q, k, pos, inv_freq, gq=None, gk=None, eps: float = 1e-6, norm:
     ldq = ldk = ldqo = ldko = 0
     mine = []
     if q is not None:
-        qp, ldq = _rows(q, "q", T, hq, D, x.dtype, dev)
+        shape = (T, hq, D)
+        qp, ldq = _rows(q, "q", shape, x.dtype, dev)
         if qo is None:
-            qo = torch.empty((T, hq, D), dtype=x.dtype, device=x.device)
+            qo = x.new_empty(shape)
             mine.append(qo)
-        qop, ldqo = _rows(qo, "qo", T, hq, D, x.dtype, dev)
+            qop, ldqo = qo.data_ptr(), hq * D
+        else:
+            qop, ldqo = _rows(qo, "qo", shape, x.dtype, dev)
     if k is not None:
-        kp, ldk = _rows(k, "k", T, hk, D, x.dtype, dev)
+        shape = (T, hk, D)
+        kp, ldk = _rows(k, "k", shape, x.dtype, dev)
         if ko is None:
-            ko = torch.empty((T, hk, D), dtype=x.dtype, device=x.device)
+            ko = x.new_empty(shape)
             mine.append(ko)
-        kop, ldko = _rows(ko, "ko", T, hk, D, x.dtype, dev)
-    _on(stream, *mine)
-    check(lib.skg_qk_norm_rope(dt, T, hq, hk, D, qp, ldq, kp, ldk, ctypes.byref(r), qop, ldqo, kop, ldko,
-                               _stream(stream)))
+            kop, ldko = ko.data_ptr(), hk * D
+        else:
+            kop, ldko = _rows(ko, "ko", shape, x.dtype, dev)
+    if stream is not None:
+        _on(stream, mine)
+    st = lib.skg_qk_norm_rope(dt, T, hq, hk, D, qp, ldq, kp, ldk, ctypes.byref(r), qop, ldqo, kop, ldko,
+                              _on_stream(stream, dev))
+    if st != OK:
+        check(st)
     return (qo if q is not None else None), (ko if k is not None else None)
 
 
@@ -198,12 +217,16 @@ def kv_store(cache: KvCache, k, v, slots, stream=None) -> None:
     slot outside it (a padded token's -1) is skipped."""
     dev = _device(k, "k")
     dt = _dtype(k, "k")
-    T = k.shape[0]
     if cache._device != dev:
         raise ValueError("the cache must be on the current GPU")
-    kp, ldk = _rows(k, "k", T, cache.heads, cache.head_dim, k.dtype, dev)
-    vp, ldv = _rows(v, "v", T, cache.heads, cache.head_dim, k.dtype, dev)
-    check(lib.skg_kv_store(cache._ref, dt, T, kp, ldk, vp, ldv, _flat(slots, "slots", T, _I64, dev), _stream(stream)))
+    T = len(k)
+    shape = (T, cache.heads, cache.head_dim)
+    kp, ldk = _rows(k, "k", shape, k.dtype, dev)
+    vp, ldv = _rows(v, "v", shape, k.dtype, dev)
+    st = lib.skg_kv_store(cache._ref, dt, T, kp, ldk, vp, ldv, _flat(slots, "slots", T, _I64, dev),
+                          _on_stream(stream, dev))
+    if st != OK:
+        check(st)
 
 
 def kv_load(cache: KvCache, slots, dtype=torch.float32, k=None, v=None, stream=None):
@@ -213,18 +236,23 @@ def kv_load(cache: KvCache, slots, dtype=torch.float32, k=None, v=None, stream=N
     T = slots.numel()
     if cache._device != dev:
         raise ValueError("the cache must be on the current GPU")
+    shape = (T, cache.heads, cache.head_dim)
     mine = []
     if k is None:
-        k = torch.empty((T, cache.heads, cache.head_dim), dtype=dtype if v is None else v.dtype, device=slots.device)
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=slots.device)
         mine.append(k)
     if v is None:
-        v = torch.empty_like(k, memory_format=torch.contiguous_format)
+        v = k.new_empty(shape)
         mine.append(v)
     dt = _dtype(k, "k")
-    kp, ldk = _rows(k, "k", T, cache.heads, cache.head_dim, k.dtype, dev)
-    vp, ldv = _rows(v, "v", T, cache.heads, cache.head_dim, k.dtype, dev)
-    _on(stream, *mine)
-    check(lib.skg_kv_load(cache._ref, dt, T, _flat(slots, "slots", T, _I64, dev), kp, ldk, vp, ldv, _stream(stream)))
+    kp, ldk = _rows(k, "k", shape, k.dtype, dev)
+    vp, ldv = _rows(v, "v", shape, k.dtype, dev)
+    if stream is not None:
+        _on(stream, mine)
+    st = lib.skg_kv_load(cache._ref, dt, T, _flat(slots, "slots", T, _I64, dev), kp, ldk, vp, ldv,
+                         _on_stream(stream, dev))
+    if st != OK:
+        check(st)
     return k, v
 
 
@@ -240,15 +268,21 @@ def qkv_rope_store(cache: KvCache, q, k, v, slots, pos, inv_freq, gq=None, gk=No
     if cache._device != dev or cache.head_dim != D:
         raise ValueError("the cache must be on the current GPU and have q's head_dim")
     r = _rope(T, hq, cache.heads, D, pos, inv_freq, gq, gk, eps, norm, interleaved, dev)
-    qp, ldq = _rows(q, "q", T, hq, D, q.dtype, dev)
-    kp, ldk = _rows(k, "k", T, cache.heads, D, q.dtype, dev)
-    vp, ldv = _rows(v, "v", T, cache.heads, D, q.dtype, dev)
+    qp, ldq = _rows(q, "q", (T, hq, D), q.dtype, dev)
+    shape = (T, cache.heads, D)
+    kp, ldk = _rows(k, "k", shape, q.dtype, dev)
+    vp, ldv = _rows(v, "v", shape, q.dtype, dev)
     if qo is None:
-        qo = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-        _on(stream, qo)
-    qop, ldqo = _rows(qo, "qo", T, hq, D, q.dtype, dev)
-    check(lib.skg_qkv_rope_store(cache._ref, dt, T, hq, qp, ldq, kp, ldk, vp, ldv, ctypes.byref(r),
-                                 _flat(slots, "slots", T, _I64, dev), qop, ldqo, _stream(stream)))
+        qo = q.new_empty((T, hq, D))
+        qop, ldqo = qo.data_ptr(), hq * D
+        if stream is not None:
+            _on(stream, [qo])
+    else:
+        qop, ldqo = _rows(qo, "qo", (T, hq, D), q.dtype, dev)
+    st = lib.skg_qkv_rope_store(cache._ref, dt, T, hq, qp, ldq, kp, ldk, vp, ldv, ctypes.byref(r),
+                                _flat(slots, "slots", T, _I64, dev), qop, ldqo, _on_stream(stream, dev))
+    if st != OK:
+        check(st)
     return qo
 
 
@@ -290,14 +324,17 @@ def tree_attn(cache: KvCache, q, table, ctx, cu=None, mask=None, max_draft: int 
     width = table.shape[1]
     if max_draft is None:
         max_draft = (T // n if n else 0) if cu is None else min(T, 64)
-    qp, ldq = _rows(q, "q", T, hq, D, q.dtype, dev)
+    shape = (T, hq, D)
+    qp, ldq = _rows(q, "q", shape, q.dtype, dev)
     mine = []
     if o is None or o is True:
-        o = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+        o = q.new_empty(shape)
         mine.append(o)
+        op, ldo = o.data_ptr(), hq * D
     elif o is False:
-        o = None
-    op, ldo = (None, 0) if o is None else _rows(o, "o", T, hq, D, q.dtype, dev)
+        o, op, ldo = None, None, 0
+    else:
+        op, ldo = _rows(o, "o", shape, q.dtype, dev)
     oqp = None
     if oq is None or oq is False:
         oq = None
@@ -307,7 +344,7 @@ def tree_attn(cache: KvCache, q, table, ctx, cu=None, mask=None, max_draft: int 
             oq = torch.empty((T, hq * D // 32, Q8_1_BLOCK_BYTES), dtype=torch.uint8, device=q.device)
             mine.append(oq)
         oqp = _flat(oq, "oq", nq, (torch.uint8,), dev)
-    size = int(lib.skg_tree_attn_workspace(cache._ref, dt, T, n, hq, max_draft, width, max_kv))
+    size = lib.skg_tree_attn_workspace(cache._ref, dt, T, n, hq, max_draft, width, max_kv)
     wp = None
     if size:
         if workspace is None:
@@ -316,10 +353,13 @@ def tree_attn(cache: KvCache, q, table, ctx, cu=None, mask=None, max_draft: int 
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on the current GPU")
         wp, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _on(stream, *mine)
-    check(lib.skg_tree_attn(
+    if stream is not None:
+        _on(stream, mine)
+    st = lib.skg_tree_attn(
         cache._ref, dt, T, n, hq, max_draft, qp, ldq, None if cu is None else _flat(cu, "cu", n + 1, _I32, dev),
         _flat(ctx, "ctx", n, _I32, dev), _flat(table, "table", n * width, _I32, dev), width, max_kv,
         None if mask is None else _flat(mask, "mask", T, _MASK, dev), 1 / math.sqrt(D) if scale is None else scale,
-        op, ldo, oqp, wp, size, _stream(stream)))
+        op, ldo, oqp, wp, size, _on_stream(stream, dev))
+    if st != OK:
+        check(st)
     return o if oq is None else (o, oq)

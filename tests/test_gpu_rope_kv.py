@@ -153,6 +153,21 @@ def expect_bytes(fmt, heads, D, page, pages, slots, x, fill=0xA5):
     return p
 
 
+# Workgroups enough for two rows a thread: a last pass that is part empty, one
+# that is all empty, and the smallest call of that kind.
+MANY_ROPE = [
+    # T, hq, hk, D, rot, interleaved, norm, bf16, pad
+    (400, 33, 6, 256, 128, False, True, True, 0),
+    (1100, 3, 1, 128, 128, True, False, False, 0),
+    (1024, 2, 0, 64, 32, False, True, False, 16),
+]
+
+
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter,norm,bf16,pad", MANY_ROPE)
+def test_qk_norm_rope_of_many_rows(skg, torch, T, hq, hk, D, rot, inter, norm, bf16, pad):
+    test_qk_norm_rope(skg, torch, T, hq, hk, D, rot, inter, norm, bf16, pad)
+
+
 CACHE = [(fmt, T, heads, D, page, bf16, pad) for fmt in oracle.KV_FMTS for T, heads, D, page, bf16, pad in
          [(1, 1, 64, 16, False, 0), (1, 32, 128, 16, False, 0), (8, 5, 256, 32, True, 16), (133, 3, 128, 64, False, 4),
           (40, 2, 64, 1024, True, 0), (17, 7, 256, 16, False, 0)]]
