@@ -223,10 +223,12 @@ __device__ inline void scaled_pair(float p0, float p1, uint32_t w0, uint32_t w1,
 }
 
 // Codes as fp16.  Two unsigned bytes in 16-bit halves are the fp16 subnormals
-// n 2^-24, which the matrix instructions take as they are: K's operand is that
-// (a high nibble is 16 n, against q / 16), and the zero of the codes is taken
-// off by the product's initial value, -zero 2^-24 sum q of the block, which is
-// constant for a row.  For V the same would leave differences of long sums, so
+// n 2^-24, which the matrix instructions take as they are: K's operand is that,
+// and the zero of the codes is taken off by the product's initial value, -zero
+// 2^-24 sum q of the block, which is constant for a row.  The instructions
+// line a subnormal's products up as if its highest bit were set, so its leading
+// zeros are lost to the sum: q4_0's nibbles are both taken as 16 n (the low one
+// as n had left scores of 2^-18 instead of 2^-22).  For V the same would leave differences of long sums, so
 // one packed fma makes (n - zero) 2^-9 of them, exactly (mul = 2^15, or 2^11
 // for a high nibble).
 __device__ inline uint32_t f16_codes(uint32_t x, float mul, float zero) {
@@ -238,9 +240,8 @@ __device__ inline uint32_t q8_pair(uint32_t x) { return f16_codes(x, 32768.f, 0.
 __device__ inline uint32_t q4_low(uint32_t x) { return f16_codes(x & 0x000F000Fu, 32768.f, 0.015625f); }
 __device__ inline uint32_t q4_high(uint32_t x) { return f16_codes(x & 0x00F000F0u, 2048.f, 0.015625f); }
 constexpr float kVScale = 512.f;          // 2^9
-constexpr float kKScale = 16777216.f;     // 2^24
-// -zero 2^-24 in both halves: of q8_0, of q4_0's low and high nibbles
-constexpr uint32_t kZero8 = 0x80808080u, kZero4Low = 0x80088008u, kZero4High = 0x80808080u;
+constexpr float kKScale8 = 16777216.f, kKScale4 = 1048576.f;  // 2^24, 2^20
+constexpr uint32_t kZero = 0x80808080u;  // two -128 2^-24
 
 // Byte y0 of w0 and byte y1 of w1, each in a 16-bit half.
 __device__ inline uint32_t two_bytes(uint32_t w0, int y0, uint32_t w1, int y1) {
@@ -509,7 +510,7 @@ __device__ inline void read_v(StepRegs<S>& r, const uint8_t* slot) {
 }
 
 // K operand of block b of tile t: elements 8g .. 8g + 7 of the block (for q4_0
-// in the order 0 2 1 3 4 6 5 7, see q_order).
+// in the order 0 2 1 3 4 6 5 7, which convert_rows gives q too).
 template <class S, int KIND, int NB>
 __device__ inline u32x4 k_operand(const StepRegs<S>& r, int t, int b) {
   u32x4 a;
@@ -528,7 +529,7 @@ __device__ inline u32x4 k_operand(const StepRegs<S>& r, int t, int b) {
     for (int i = 0; i < 4; i += 2) {  // bytes i NB + b and (i + 1) NB + b
       const int y0 = i * NB + b, y1 = (i + 1) * NB + b;
       const uint32_t x = two_bytes(r.k[t][y0 >> 2], y0 & 3, r.k[t][y1 >> 2], y1 & 3);
-      a[i] = S::kSubnormal ? x & 0x000F000Fu : q4_low(x);
+      a[i] = S::kSubnormal ? (x << 4) & 0x00F000F0u : q4_low(x);
       a[i + 1] = S::kSubnormal ? x & 0x00F000F0u : q4_high(x);
     }
   }
@@ -874,7 +875,7 @@ __device__ inline float convert_rows(const RawRows<T, D>& raw, float scale, Put&
     int e = int((__builtin_bit_cast(uint32_t, amax) >> 23) & 255);  // |q| < 2^(e - 126)
     e = e < 40 ? 40 : (e > 220 ? 220 : e);
     to *= pow2(14 - (e - 126));
-    rs *= (S::kSubnormal ? kKScale : kVScale) * pow2(e - 126 - 14);
+    rs *= (!S::kSubnormal ? kVScale : KIND == KV_Q8_0 ? kKScale8 : kKScale4) * pow2(e - 126 - 14);
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -883,9 +884,8 @@ __device__ inline float convert_rows(const RawRows<T, D>& raw, float scale, Put&
     for (int j = 0; j < 4; ++j) {
       // q4_0's operand order: 0 2 1 3 4 6 5 7
       const int i0 = KIND == KV_Q4_0 ? 4 * (j >> 1) + (j & 1) : 2 * j, i1 = KIND == KV_Q4_0 ? i0 + 2 : 2 * j + 1;
-      const float f = KIND == KV_Q4_0 && S::kSubnormal && (j & 1) ? to * 0.0625f : to;  // against high nibbles
       uint32_t t[NT];
-      split_pair<S::kF16, NT>(x[b][i0] * f, x[b][i1] * f, t);
+      split_pair<S::kF16, NT>(x[b][i0] * to, x[b][i1] * to, t);
 #pragma unroll
       for (int k = 0; k < NT; ++k) w[k][j] = t[k];
     }
@@ -947,7 +947,7 @@ __device__ inline void finish(const TreeArgs& a, int64_t tok, int64_t at, float 
 // The products' initial values: minus the zero of the codes times the row's q.
 template <class S, int KIND, int NB, int NT, class W>
 __device__ inline void fill_zero(W& w) {
-  const u32x4 z = KIND == KV_Q8_0 ? u32x4{kZero8, kZero8, kZero8, kZero8} : u32x4{kZero4Low, kZero4High, kZero4Low, kZero4High};
+  const u32x4 z{kZero, kZero, kZero, kZero};
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     w.zero[b] = f32x4{0.f, 0.f, 0.f, 0.f};

@@ -381,3 +381,22 @@ def test_decode_layer_chain(skg, torch):
     assert np.all(np.abs(host(o) - ref) <= tol)
     yr, b = oracle.gemv_q8_0_q8_1_ref(W[3], host(oq).reshape(M, -1, 36))
     assert oracle.check_close(y, yr, oracle.tolerance(b))[0]
+
+
+@pytest.mark.parametrize("fmt", oracle.KV_FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3, 24, 61])
+def test_float32_rows_keep_float32_scores(skg, torch, fmt, D, n):
+    """Random rows of 64 query heads that see two keys (n = 1) or their own and
+    those before: what the bounds over all roundings above leave, their root
+    mean square does not.  A score's: q in two terms of 11 bits is off by 2^-23
+    relative to each of D products of about 2 / sqrt(D), 2^-22 altogether; a
+    block's sum of codes times q is about 128 * 2 * sqrt(32) steps of amax / 127
+    = 2.2 / 127, 25 of values, rounded to 2^-24 in each of four additions of
+    D / 32 blocks, over sqrt(D): 2^-21.4; for the bf16 cache less.  It reaches
+    o as p (1 - p) |v - v'| <= 0.35 of that, below 2^-22.5 with the 2^-23.5 of
+    p and v.  A quarter of that margin is left to spare."""
+    note(f"tree_attn precision {fmt} D={D} n={n}")
+    p = Problem(skg, torch, fmt, [1 if n == 1 else 3], [n], 64, 64 if n == 1 else 8, D, 16, masks=None, qs=2.0, seed=5)
+    o, want = p.run().astype(np.float64), p.reference()[0]
+    assert np.sqrt(np.mean((o - want) ** 2)) <= 2.0**-20
