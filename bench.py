@@ -428,7 +428,9 @@ LAYER_MODES = {
     "norm_fused": ("_rmsnorm_fused", 4),
     "full_unfused": ("_full_rmsnorm_unfused", 10),
     "full_fused": ("_full_rmsnorm_fused", 7),
+    "attn": ("_attention_4k", 9),
 }
+LAYER_CONTEXT = 4087  # keys before the token, in the "attn" mode
 
 
 def bench_layer(skg, si, torch, timer, warm_s, mode="plain"):
@@ -448,9 +450,14 @@ def bench_layer(skg, si, torch, timer, warm_s, mode="plain"):
         (attention, then feed-forward).  Attention and the residual adds are
         not part of the path: O reads the Q8_1 blocks of a fixed stand-in for
         the attention output, quantised each layer, and the second norm reads
-        a fixed stand-in for the residual stream."""
+        a fixed stand-in for the residual stream.
+      attn (9): full_fused with the attention itself: rotation of q and k and
+        the store of k and v into a paged q8_0 cache (one launch), attention
+        over the 4087 keys before the token and itself, whose join writes the
+        Q8_1 blocks that O reads (two launches).  Each layer has a cache of its
+        own, 36 MB."""
     suffix, launches = LAYER_MODES[mode]
-    full = mode.startswith("full")
+    full = mode in ("full_unfused", "full_fused", "attn")
     D, F = 4096, 11008
     fmt = skg.Q4_0_Q8_1
     layers = []
@@ -491,6 +498,36 @@ def bench_layer(skg, si, torch, timer, warm_s, mode="plain"):
     eps = 1e-5
     xqb, hqb = D // 32 * 36, F // 32 * 36
 
+    attention = []
+    if mode == "attn":
+        H, HD, page, total = 32, 128, 64, LAYER_CONTEXT + 1
+        pages = -(-total // page)
+        f32 = skg.kv.F32
+        table = torch.randperm(pages, device="cuda", dtype=torch.int64).to(torch.int32).view(1, pages)
+        at = torch.arange(total, device="cuda")
+        slots = table[0].to(torch.int64)[at // page] * page + at % page
+        here, pos = slots[-1:].clone(), torch.tensor([LAYER_CONTEXT], dtype=torch.int32, device="cuda")
+        ctx = pos.clone()
+        inv_freq = (10000.0 ** (-torch.arange(0, HD, 2, device="cuda", dtype=torch.float64) / HD)).to(torch.float32)
+        gen = torch.Generator(device="cuda").manual_seed(17)
+        caches = []
+        for _ in range(32):
+            c = skg.kv_cache(skg.KV_Q8_0, H, HD, page, pages)
+            skg.kv_store(c, *(torch.randn((total, H, HD), device="cuda", generator=gen) for _ in range(2)), slots)
+            caches.append(c)
+        rope = skg.kv.rope_args(HD, pos, inv_freq, interleaved=True)
+        size = skg.tree_attn_workspace(caches[0], torch.float32, 1, 1, H, 1, pages)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        refs = [skg.kv.cache_args(c) for c in caches]
+        yqp, ykp, yvp, wsp, scale = yq.data_ptr(), yk.data_ptr(), yv.data_ptr(), ws.data_ptr(), HD ** -0.5
+        slotp, ctxp, tabp = here.data_ptr(), ctx.data_ptr(), table.data_ptr()
+        row = 2 * D * 34 // 32  # a token's keys and values in the cache
+        attention = [
+            (lambda i, s: lib.skg_qkv_rope_store(refs[i], f32, 1, H, yqp, D, ykp, D, yvp, D, rope, slotp, yqp, D, s),
+             4 * 4 * D + row),
+            (lambda i, s: lib.skg_tree_attn(refs[i], f32, 1, 1, H, 1, yqp, D, None, ctxp, tabp, pages, 0, None, scale,
+                                            None, 0, aqp, wsp, size, s), total * row + 4 * D + xqb)]
+
     # Each step: (function of (layer, stream), algorithmic bytes read + written).
     def quantize(src, dst, K, qb):
         return (lambda i, s: lib.skg_quantize_act_q8_1(1, K, src, dst, s), 4 * K + qb)
@@ -518,16 +555,18 @@ def bench_layer(skg, si, torch, timer, warm_s, mode="plain"):
                          norm_fp32(x2p, 1), quantize(xnp, xqp, D, xqb), swiglu, quantize(hp, hqp, F, hqb), down],
         "full_fused": [norm_q8_1(xp, 0), qkv, quantize(attp, aqp, D, xqb), oproj, norm_q8_1(x2p, 1), swiglu_q,
                        down],
+        "attn": [norm_q8_1(xp, 0), qkv, *attention, oproj, norm_q8_1(x2p, 1), swiglu_q, down],
     }
     chain = chains[mode]
-    assert len(chain) == launches
+    assert len(chain) + (mode == "attn") == launches  # the attention's join is a launch of its call
     fns = [f for f, _ in chain]
 
     def launch(i, sh):
         for f in fns:
             f(i, sh)
 
-    launch(0, sh)
+    for f in fns:
+        skg.check(f(0, sh))
     torch.cuda.synchronize()
     if not bool(torch.isfinite(yo).all()) or (full and not bool(torch.isfinite(ya).all())):
         raise RuntimeError("layer chain produced non-finite output")
@@ -543,6 +582,13 @@ def bench_layer(skg, si, torch, timer, warm_s, mode="plain"):
     res["frac_peak"] = res["gbs"] / PEAK_HBM_GBS
     res["graph"] = bench_graph(torch, launch, 32, per_graph=32)
     res["graph"]["gbs"] = alg / (res["graph"]["us_per_launch"] * 1e-6) / 1e9
+    if mode == "attn":  # the two calls alone
+        def attend(i, sh):
+            for f, _ in attention:
+                f(i, sh)
+        r = timer.run(attend, 32, repeats=20, per_repeat=32, warm_s=warm_s)
+        res["attention"] = dict(us=r["us_per_launch"], graph=bench_graph(torch, attend, 32, per_graph=32),
+                                algorithmic_bytes=sum(b for _, b in attention), keys=total)
     del layers
     torch.cuda.empty_cache()
     return res
@@ -962,6 +1008,10 @@ def main():
             details["arms"][r["name"]] = r
             log(f"[{r['name']}] {r['us_per_layer']:.2f} us/layer {r['gbs']:.0f} GB/s  graph "
                 f"{r['graph']['us_per_launch']:.2f} us/layer ({r['graph']['gbs']:.0f} GB/s)")
+            if "attention" in r:
+                a = r["attention"]
+                log(f"    rotation, store and attention over {a['keys']} keys: {a['us']:.2f} us  graph "
+                    f"{a['graph']['us_per_launch']:.2f} us")
     if "prefill" in arms:
         for kind, act in (("q4_0", "bf16"), ("q8_0", "bf16"), ("q4_K", "bf16"), ("q6_K", "bf16"),
                           ("q4_0", "q8_1"), ("q8_0", "q8_1")):

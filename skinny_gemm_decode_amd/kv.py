@@ -19,7 +19,8 @@ from . import OK, Q8_1_BLOCK_BYTES, _stream, check, lib
 # skg_kv_fmt
 KV_BF16, KV_Q8_0, KV_Q4_0 = range(3)
 # skg_dtype
-_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+F32, BF16 = range(2)
+_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 class _Cache(ctypes.Structure):
@@ -162,6 +163,19 @@ def _rope(T: int, hq: int, hk: int, D: int, pos, inv_freq, gq, gk, eps: float, n
         if gk is not None and hk:
             r.gk = _flat(gk, "gk", D, _F32, dev)
     return r
+
+
+def cache_args(cache: KvCache):
+    """The skg_kv_cache argument of direct calls of ``lib`` (by reference)."""
+    return cache._ref
+
+
+def rope_args(head_dim: int, pos, inv_freq, gq=None, gk=None, eps: float = 1e-6, norm: bool = False,
+              interleaved: bool = False):
+    """The skg_rope argument of direct calls of ``lib`` (by reference), for
+    pos.numel() tokens; the tensors have to outlive it."""
+    return ctypes.byref(_rope(pos.numel(), 1, 1, head_dim, pos, inv_freq, gq, gk, eps, norm, interleaved,
+                              _device(pos, "pos")))
 
 
 def qk_norm_rope(q, k, pos, inv_freq, gq=None, gk=None, eps: float = 1e-6, norm: bool = False,
