@@ -269,7 +269,7 @@ size_t skg_tree_attn_workspace(const skg_kv_cache* cache, skg_dtype dtype, int64
   if (check_dtype(dtype) != SKG_OK || check_cache(cache, &c, &bytes, false) != SKG_OK) return 0;
   if (check_attn(cache, T, n_seqs, hq, max_draft, width, &max_kv) != SKG_OK) return 0;
   ok();
-  return tree_attn_workspace(cache->head_dim, cache->heads, dtype, T, n_seqs, hq, max_draft, max_kv);
+  return tree_attn_workspace(cache->fmt, cache->head_dim, cache->heads, dtype, T, n_seqs, hq, max_draft, max_kv);
 }
 
 skg_status skg_tree_attn(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, int64_t n_seqs, int hq,
@@ -304,7 +304,7 @@ skg_status skg_tree_attn(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, 
     if (overlap_bytes(sq, T, dtype, oq, nq) || (o && overlap_bytes(so, T, dtype, oq, nq)))
       return fail(SKG_E_INVALID_ARG, "oq overlaps q or o");
   }
-  const size_t need = tree_attn_workspace(cache->head_dim, cache->heads, dtype, T, n_seqs, hq, max_draft, max_kv);
+  const size_t need = tree_attn_workspace(cache->fmt, cache->head_dim, cache->heads, dtype, T, n_seqs, hq, max_draft, max_kv);
   if (need) {
     if (!ws || ws_bytes < need)
       return fail(SKG_E_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, ws ? ws_bytes : size_t(0));

@@ -43,7 +43,7 @@ hipError_t launch_qkv_rope_store(const KvView& c, int kind, int D, skg_dtype dt,
                                  const skg_rope* rope, const int64_t* slots, void* qo, int64_t ldqo,
                                  hipStream_t stream);
 struct TreeArgs;
-size_t tree_attn_workspace(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft,
+size_t tree_attn_workspace(int kind, int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft,
                            int64_t max_kv);
 hipError_t launch_tree_attn(const TreeArgs& a, int kind, int D, skg_dtype dt, int heads, void* ws,
                             hipStream_t stream);

@@ -137,11 +137,34 @@ AttnForm form_of(int D, skg_dtype dt, int64_t rows) {
 }
 constexpr int kTileOf[] = {16, 32, 64, 128, 256};
 
-// Splits: two workgroups of four waves (one of eight) for each of 256 CUs,
-// counted over all heads, row groups and sequences; where there are that many
-// without splitting, four times as many, so that long sequences do not stand
-// alone at the end.  More than 256 sequences are not split.
-Plan plan(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
+// Workgroups of a form that a CU holds at once.
+template <int KIND, int D, int NT>
+int per_cu(AttnForm f) {
+  if (f == kKeys1) return AttnShape<KIND, D, NT, 1, 4, false>::kPerCu;
+  if constexpr (D <= 128)
+    if (f == kKeys2) return AttnShape<KIND, D, NT, 2, 4, false>::kPerCu;
+  return f == kRows64 ? AttnShape<KIND, D, NT, 1, 4, true>::kPerCu : 1;
+}
+template <int KIND, int D>
+int per_cu(AttnForm f, skg_dtype dt) {
+  return dt == SKG_F32 ? per_cu<KIND, D, KIND == KV_BF16 ? 3 : 2>(f) : per_cu<KIND, D, 1>(f);
+}
+template <int KIND>
+int per_cu(AttnForm f, int D, skg_dtype dt) {
+  return D == 64 ? per_cu<KIND, 64>(f, dt) : D == 128 ? per_cu<KIND, 128>(f, dt) : per_cu<KIND, 256>(f, dt);
+}
+
+// Splits: as many workgroups as 256 CUs hold, counted over all heads, row
+// groups and sequences (at D = 256, where a CU holds one, twice as many took
+// 38 us for 60000 keys, this 28.8).  Where there are half that many without
+// splitting, twice as many, so that long sequences do not stand alone at the
+// end: 64 q8_0 sequences of up to 2000 keys 37.7 us, with as many as the CUs
+// hold 39.9, with four times as many 45.4; bf16 47.1, 53.2 and 48.7.  A single
+// sequence splits evenly, and where its steps are 8 KB one workgroup's copies
+// keep a CU busy (q8_0 of 128 elements: 131071 keys 51.9 us with one, 54.6 with
+// two; sixteen ragged sequences 36.1 and 32.9; a single one in steps of half
+// that 49.3 and 42.7).  More than 256 sequences are not split.
+Plan plan(int kind, int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft, int64_t max_kv) {
   Plan p;
   const int64_t rows = int64_t(max_draft) * (hq / heads);
   p.form = form_of(D, dt, rows);
@@ -151,8 +174,11 @@ Plan plan(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int
   const int64_t steps = (max_kv + kStep - 1) / kStep, each = (steps + kMinSteps - 1) / kMinSteps;
   int64_t want = 0;
   if (n_seqs <= kMaxSplitSeqs && each > 1) {
-    const int64_t full = p.form >= kRows128 ? 256 : 512;
-    const int64_t fill = lanes * n_seqs <= full / 2 ? full : 4 * full;
+    const int fits = kind == KV_BF16   ? per_cu<KV_BF16>(p.form, D, dt)
+                     : kind == KV_Q8_0 ? per_cu<KV_Q8_0>(p.form, D, dt)
+                                       : per_cu<KV_Q4_0>(p.form, D, dt);
+    const int64_t full = 256 * (n_seqs == 1 && kv_row_bytes(kind, D) >= 128 ? 1 : fits);
+    const int64_t fill = lanes * n_seqs <= full / 2 ? full : 2 * full;
     want = fill / lanes - n_seqs / 2;
     want = want < 1 ? 1 : want;
   }
@@ -171,15 +197,15 @@ Plan plan(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int
 
 }  // namespace
 
-size_t tree_attn_workspace(int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft,
+size_t tree_attn_workspace(int kind, int D, int heads, skg_dtype dt, int64_t T, int64_t n_seqs, int hq, int max_draft,
                            int64_t max_kv) {
-  return plan(D, heads, dt, T, n_seqs, hq, max_draft, max_kv).bytes;
+  return plan(kind, D, heads, dt, T, n_seqs, hq, max_draft, max_kv).bytes;
 }
 
 hipError_t launch_tree_attn(const TreeArgs& args, int kind, int D, skg_dtype dt, int heads, void* ws,
                             hipStream_t stream) {
   TreeArgs a = args;
-  const Plan p = plan(D, heads, dt, a.T, a.n_seqs, a.hq, a.max_draft, a.max_kv);
+  const Plan p = plan(kind, D, heads, dt, a.T, a.n_seqs, a.hq, a.max_draft, a.max_kv);
   a.want = p.want;
   a.row_groups = p.row_groups;
   a.tile = kTileOf[p.form];
