@@ -59,6 +59,7 @@ struct TreeArgs {
   int64_t blocks;    // Q8_1 blocks of a token's row
   int per_seq;       // T / n_seqs
   int want;          // splits to make of all sequences' keys together; 0: each sequence is one
+  int cost_shift;    // unit of a sequence's cost (2^cost_shift steps), so that the sum fits 31 bits
   int row_groups;    // workgroups along a sequence's rows
   int tile;          // rows of a workgroup
   float* sums;       // partial results: [split][row group][head][tile][D]
@@ -81,10 +82,12 @@ __device__ inline int wave_sum_int(int v) {
 }
 __device__ inline int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// Splits are of equal length over all sequences: per = the steps of all of
-// them over the splits that are wanted, so a long sequence gets many and a
-// short one gets one, and a workgroup finds its own from the lengths, one lane
-// a sequence.
+// Splits are of equal cost over all sequences: per = the cost of all of them
+// over the splits that are wanted, so a long sequence gets many and a short one
+// gets one, and a workgroup finds its own from the lengths, one lane a sequence.
+// A step costs 1, or 2 where 256 rows share it (WEIGH) and more than half of
+// them are there (four sequences of 61, 61, 6 and 23 drafted tokens 47.9 us
+// without that, 43.4 with it; with 128 rows of three terms it cost 1.3 of 33).
 struct Splits {  // of 64 sequences, one a lane
   KvSpan sp;
   int n, incl;  // splits of the sequence; of it and all before it
@@ -95,20 +98,36 @@ __device__ __forceinline__ Splits lane_span(const TreeArgs& a, int b) {
   return s;
 }
 __device__ inline int steps_of(const KvSpan& sp) { return sp.keys / kStep + (sp.keys % kStep != 0); }
-// Steps of a split.
-__device__ __forceinline__ int split_steps(const TreeArgs& a, const Splits& first) {
-  int total = steps_of(first.sp);
+template <bool WEIGH>
+__device__ inline int dear(const TreeArgs& a, const KvSpan& sp) {
+  return WEIGH && 2 * sp.n * a.group > a.tile;
+}
+template <bool WEIGH>
+__device__ inline int cost_of(const TreeArgs& a, const KvSpan& sp) {
+  return sp.n == 0 ? 0 : ((steps_of(sp) << dear<WEIGH>(a, sp)) + (1 << a.cost_shift) - 1) >> a.cost_shift;
+}
+// Cost of a split.
+template <bool WEIGH>
+__device__ __forceinline__ int split_cost(const TreeArgs& a, const Splits& first) {
+  int total = cost_of<WEIGH>(a, first.sp);
   if (a.n_seqs > 1) {
 #pragma unroll 1
-    for (int b = 64; b < a.n_seqs; b += 64) total += steps_of(lane_span(a, b + (threadIdx.x & 63)).sp);
+    for (int b = 64; b < a.n_seqs; b += 64) total += cost_of<WEIGH>(a, lane_span(a, b + (threadIdx.x & 63)).sp);
     total = wave_sum_int(total);
   }
   total = __builtin_amdgcn_readfirstlane(total);
-  const int per = total / a.want + (total % a.want != 0);
+  return total / a.want + (total % a.want != 0);
+}
+// Steps of a split of a sequence.
+template <bool WEIGH>
+__device__ __forceinline__ int split_steps(const TreeArgs& a, const KvSpan& sp, int cost) {
+  const int d = dear<WEIGH>(a, sp), most = (1 << 27) >> a.cost_shift;
+  const int per = (((cost < most ? cost : most) << a.cost_shift) + d) >> d;
   return per < kMinSteps ? kMinSteps : per;
 }
-__device__ __forceinline__ void count_splits(const TreeArgs& a, Splits& s, int per, int before) {
-  const int n = (steps_of(s.sp) + per - 1) / per;
+template <bool WEIGH>
+__device__ __forceinline__ void count_splits(const TreeArgs& a, Splits& s, int cost, int before) {
+  const int per = split_steps<WEIGH>(a, s.sp, cost), n = (steps_of(s.sp) + per - 1) / per;
   s.n = s.sp.n == 0 ? 0 : n < 1 ? 1 : n;
   int incl = s.n;
   if (a.n_seqs > 1) {
@@ -128,6 +147,7 @@ struct Unit {
   int seq, begin, end, splits, base;
 };
 // Split u of all (by_seq: the splits of sequence u); false if there is none.
+template <bool WEIGH>
 __device__ __forceinline__ bool find_unit(const TreeArgs& a, int u, Unit& w, bool by_seq = false) {
   if (a.want == 0) {
     w.seq = u;
@@ -140,12 +160,12 @@ __device__ __forceinline__ bool find_unit(const TreeArgs& a, int u, Unit& w, boo
   }
   const int lane = threadIdx.x & 63;
   Splits s = lane_span(a, lane);
-  const int per = split_steps(a, s);
+  const int cost = split_cost<WEIGH>(a, s);
   int before = 0;  // splits of the sequences of earlier rounds
 #pragma unroll 1
   for (int b0 = 0; b0 < a.n_seqs; b0 += 64) {
     if (b0) s = lane_span(a, b0 + lane);
-    count_splits(a, s, per, before);
+    count_splits<WEIGH>(a, s, cost, before);
     const uint64_t hit = __ballot(by_seq ? b0 + lane == u : s.incl > u && s.n > 0);
     if (hit) {
       const int b = __builtin_ctzll(hit);
@@ -153,6 +173,7 @@ __device__ __forceinline__ bool find_unit(const TreeArgs& a, int u, Unit& w, boo
       w.splits = lane_of(s.n, b);
       w.base = lane_of(s.incl, b) - w.splits;
       w.sp = KvSpan{lane_of(s.sp.t0, b), lane_of(s.sp.ctx, b), lane_of(s.sp.n, b), lane_of(s.sp.keys, b)};
+      const int per = split_steps<WEIGH>(a, w.sp, cost);
       w.begin = (u - w.base) * per;
       const int all = steps_of(w.sp);
       w.end = w.begin + per < all ? w.begin + per : all;
@@ -998,7 +1019,7 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
   const int c = lane & 15, g = lane >> 4;
 
   Unit unit;
-  if (!find_unit(a, blockIdx.y, unit)) return;
+  if (!find_unit<false>(a, blockIdx.y, unit)) return;
   const KvSpan sp = unit.sp;
   const int first = rg * 16 * RT, rows = sp.n * a.group;
   if (first >= rows) return;
@@ -1182,7 +1203,7 @@ __global__ __launch_bounds__(64 * W, (W == 8 ? 2 : AttnShape<KIND, D, NT, RT, W,
   const int c = lane & 15, g = lane >> 4;
 
   Unit unit;
-  if (!find_unit(a, blockIdx.y, unit)) return;
+  if (!find_unit<RT * W == 16>(a, blockIdx.y, unit)) return;
   const KvSpan sp = unit.sp;
   const int rows = sp.n * a.group, group_first = rg * 16 * RT * W;
   if (group_first >= rows) return;

@@ -13,7 +13,7 @@ namespace {
 // CUs: the last workgroup to arrive joining them (write-through stores and a
 // counter) took 3.3 us where this takes 3.9 with its launch at 16 splits of 8
 // rows, but 8 where this takes 5 at 64, and needed a workspace kept at zero.
-template <class T, int D, int SUBS>
+template <class T, int D, int SUBS, bool WEIGH>
 __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeArgs a, float unit) {
   constexpr int B = D / 32, kDeep = 4;
   __shared__ __attribute__((aligned(16))) float buf[SUBS > 4 ? 4 : 1][D];
@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeArgs a, float u
   const int sub = SUBS > 4 ? threadIdx.x >> 4 : (threadIdx.x >> 4) & 3;
   const int h = SUBS > 4 ? blockIdx.x : 4 * blockIdx.x + wave, i = blockIdx.y;
   Unit unit_of;
-  if (!find_unit(a, blockIdx.z, unit_of, true)) return;
+  if (!find_unit<WEIGH>(a, blockIdx.z, unit_of, true)) return;
   const KvSpan sp = unit_of.sp;
   const int splits = unit_of.splits, before = unit_of.base;
   if (i >= sp.n || splits <= 1 || h >= a.hq) return;  // uniform over a wave, with SUBS > 4 over the workgroup
@@ -103,13 +103,14 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeArgs a, float u
 
 template <class T, int D>
 hipError_t join(const TreeArgs& a, float unit, bool wide, hipStream_t stream) {
-  if (wide)
-    hipLaunchKernelGGL((tree_attn_join_kernel<T, D, 16>), dim3(unsigned(a.hq), unsigned(a.max_draft), unsigned(a.n_seqs)),
+  auto launch = [&](auto kernel, int heads) {  // heads of a workgroup
+    hipLaunchKernelGGL(kernel, dim3(unsigned((a.hq + heads - 1) / heads), unsigned(a.max_draft), unsigned(a.n_seqs)),
                        dim3(256), 0, stream, a, unit);
-  else
-    hipLaunchKernelGGL((tree_attn_join_kernel<T, D, 4>), dim3(unsigned((a.hq + 3) / 4), unsigned(a.max_draft), unsigned(a.n_seqs)),
-                       dim3(256), 0, stream, a, unit);
-  return hipGetLastError();
+    return hipGetLastError();
+  };
+  if (a.tile > 128)
+    return wide ? launch(tree_attn_join_kernel<T, D, 16, true>, 1) : launch(tree_attn_join_kernel<T, D, 4, true>, 4);
+  return wide ? launch(tree_attn_join_kernel<T, D, 16, false>, 1) : launch(tree_attn_join_kernel<T, D, 4, false>, 4);
 }
 template <class T>
 hipError_t join_dim(const TreeArgs& a, int D, float unit, bool wide, hipStream_t s) {
@@ -207,6 +208,8 @@ hipError_t launch_tree_attn(const TreeArgs& args, int kind, int D, skg_dtype dt,
   TreeArgs a = args;
   const Plan p = plan(kind, D, heads, dt, a.T, a.n_seqs, a.hq, a.max_draft, a.max_kv);
   a.want = p.want;
+  a.cost_shift = 0;
+  while ((((a.max_kv + kStep - 1) / kStep * 2) >> a.cost_shift) + 1 > INT32_MAX / a.n_seqs) ++a.cost_shift;
   a.row_groups = p.row_groups;
   a.tile = kTileOf[p.form];
   a.per_seq = int(a.T / a.n_seqs);
