@@ -27,7 +27,6 @@ struct Elem<float> {
     for (int i = 0; i < 4; ++i) u[i] = __builtin_bit_cast(uint32_t, x[i]);
     return u;
   }
-  __device__ static f32x2 pair(const void* p) { return *static_cast<const f32x2*>(p); }
   __device__ static void put_pair(void* p, float a, float b) { *static_cast<f32x2*>(p) = f32x2{a, b}; }
 };
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -51,10 +50,6 @@ struct Elem<__bf16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
     return u;
-  }
-  __device__ static f32x2 pair(const void* p) {
-    const uint32_t u = *static_cast<const uint32_t*>(p);
-    return f32x2{bf16_lo(u), bf16_hi(u)};
   }
   __device__ static void put_pair(void* p, float a, float b) { *static_cast<uint32_t*>(p) = bf16_pair(a, b); }
 };

@@ -15,10 +15,10 @@
 // no exchange (lanes past the rotated part hold two adjacent units).  The sum
 // of squares meets over the row's 4..32 lanes.
 //
-// Cache rows.  The encoder gives a lane the element pair (2c, 2c + 1) of blocks
-// 2 bp and 2 bp + 1, c = lane & 15: the loads of a 16-lane row are 128
-// contiguous bytes of binary32, a block's maximum is four DPP steps, and the
-// lane's four codes are adjacent in the cache row.
+// Cache rows.  The encoder and the decoder give a lane 16 bytes of the row in
+// each of two adjacent blocks: the row's accesses are whole, a block's maximum
+// is two or three DPP steps, and the codes of a column's two blocks are
+// adjacent in the cache row.
 #include "kv_common.h"
 #include "kernels.h"
 
@@ -34,18 +34,18 @@ __device__ inline int dpp_u(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
 }
 
-// Largest value / smallest integer over the 16 lanes of a DPP row, in all of them.
-__device__ inline float row16_max(float v) {
+// Largest value / smallest integer over aligned groups of L lanes (4 or 8), in all of them.
+template <int L>
+__device__ inline float group_max(float v) {
   v = fmaxf(v, dpp_f<SKG_DPP_QUAD_XOR1>(v));
   v = fmaxf(v, dpp_f<SKG_DPP_QUAD_XOR2>(v));
-  v = fmaxf(v, dpp_f<SKG_DPP_ROW_HALF_MIRROR>(v));
-  return fmaxf(v, dpp_f<SKG_DPP_ROW_MIRROR>(v));
+  return L == 8 ? fmaxf(v, dpp_f<SKG_DPP_ROW_HALF_MIRROR>(v)) : v;
 }
-__device__ inline int row16_min(int v) {
+template <int L>
+__device__ inline int group_min(int v) {
   v = min(v, dpp_u<SKG_DPP_QUAD_XOR1>(v));
   v = min(v, dpp_u<SKG_DPP_QUAD_XOR2>(v));
-  v = min(v, dpp_u<SKG_DPP_ROW_HALF_MIRROR>(v));
-  return min(v, dpp_u<SKG_DPP_ROW_MIRROR>(v));
+  return L == 8 ? min(v, dpp_u<SKG_DPP_ROW_HALF_MIRROR>(v)) : v;
 }
 // Sum over aligned groups of L lanes (a power of two, 4..32), in all of them.
 template <int L>
@@ -224,10 +224,13 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(Rows q, Rows k, 
 
 // ---- cache rows -------------------------------------------------------------
 
-template <int D>
-struct PairShape {
-  static constexpr int kLanes = D / 4;              // lanes of a row
-  static constexpr int kRows = kThreads / kLanes;   // rows of a pass
+// Lane (j, bp) of a row has V elements, V j .. V j + V - 1, of each of blocks
+// 2 bp and 2 bp + 1: 16 bytes of a row in memory.
+template <int V, int D>
+struct UnitShape {
+  static constexpr int kBlock = 32 / V;              // lanes of a block
+  static constexpr int kLanes = kBlock * (D / 64);   // of a row
+  static constexpr int kRows = kThreads / kLanes;    // rows of a workgroup
 };
 
 __device__ inline int round_code(float x, float id, int lo, int hi) {
@@ -238,66 +241,66 @@ __device__ inline uint32_t scale16(float d) {
   return __half_as_ushort(__float2half_rn(fminf(fmaxf(d, -65504.f), 65504.f)));
 }
 
-// One block's pair (x, y) = elements 2c, 2c + 1 from each of 16 lanes: the
-// codes (x low) and the scale.  q8_0 codes are offset by 128, q4_0's by 8.
-template <int KIND>
-__device__ inline void encode_pair(float x, float y, int c, uint32_t& qx, uint32_t& qy, uint32_t& s) {
+// One block, V elements from each of 32 / V lanes: the codes and the scale.
+// q8_0 codes are offset by 128, q4_0's by 8.
+template <int KIND, int V>
+__device__ inline void encode_block(const float (&x)[V], int j, uint32_t (&q)[V], uint32_t& s) {
 #pragma clang fp contract(off)
-  const float ax = fabsf(x), ay = fabsf(y), amax = row16_max(fmaxf(ax, ay));
+  float amax = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < V; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  amax = group_max<32 / V>(amax);
+  float d;
   if constexpr (KIND == KV_Q8_0) {
-    const float d = amax / 127.0f, id = q8_1_id(d);
-    qx = uint32_t(round_code(x, id, -127, 127) + 128);
-    qy = uint32_t(round_code(y, id, -127, 127) + 128);
-    s = scale16(d);
+    d = amax / 127.0f;
   } else {
     // the first element of magnitude amax: its index and, in bit 0, its sign
-    const int ix = ax == amax ? 4 * c + int(__float_as_uint(x) >> 31) : 4096;
-    const int iy = ay == amax ? 4 * c + 2 + int(__float_as_uint(y) >> 31) : 4096;
-    const int at = row16_min(min(ix, iy));
-    const float m = (at & 1) ? -amax : amax;
-    const float d = m / -8.0f, id = q8_1_id(d);
-    qx = uint32_t(round_code(x, id, -8, 7) + 8);
-    qy = uint32_t(round_code(y, id, -8, 7) + 8);
-    s = scale16(d);
+    int at = 4096;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) at = fabsf(x[i]) == amax ? 2 * (V * j + i) + int(__float_as_uint(x[i]) >> 31) : at;
+    d = ((group_min<32 / V>(at) & 1) ? -amax : amax) / -8.0f;
   }
+  const float id = q8_1_id(d);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    q[i] = uint32_t(KIND == KV_Q8_0 ? round_code(x[i], id, -127, 127) + 128 : round_code(x[i], id, -8, 7) + 8);
+  s = scale16(d);
 }
 
-// A cache row from its D / 4 lanes: lane (c, bp) holds x = elements 2c, 2c + 1
-// of block 2 bp and y those of block 2 bp + 1.  chunk: the (page, head)'s.
-template <int KIND, int D>
-__device__ inline void put_row(uint8_t* chunk, uint32_t shift, uint32_t tok, int c, int bp, f32x2 x, f32x2 y,
-                               bool store) {
+// A cache row from its lanes (see UnitShape).  chunk: the (page, head)'s.
+template <int KIND, int D, int V>
+__device__ inline void put_units(uint8_t* chunk, uint32_t shift, uint32_t tok, int j, int bp, const float (&x)[V],
+                                 const float (&y)[V], bool store) {
   uint8_t* row = chunk + kv_codes_at(KIND, D, tok);
   if constexpr (KIND == KV_BF16) {
     if (store) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(row) + 32 * bp + c;
-      w[0] = bf16_pair(x.x, x.y);
-      w[16] = bf16_pair(y.x, y.y);
+      uint32_t* w = reinterpret_cast<uint32_t*>(row) + 32 * bp + V / 2 * j;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+        w[16 + i] = bf16_pair(y[2 * i], y[2 * i + 1]);
+      }
     }
   } else {
     constexpr int NB = D / 32;
-    uint32_t a0, a1, b0, b1, s0, s1;
-    encode_pair<KIND>(x.x, x.y, c, a0, a1, s0);
-    encode_pair<KIND>(y.x, y.y, c, b0, b1, s1);
+    uint32_t a[V], b[V], s0, s1;
+    encode_block<KIND, V>(x, j, a, s0);
+    encode_block<KIND, V>(y, j, b, s1);
     if (store) {
-      if constexpr (KIND == KV_Q8_0)
-        *reinterpret_cast<uint32_t*>(row + 2 * NB * c + 4 * bp) = a0 | (a1 << 8) | (b0 << 16) | (b1 << 24);
-      else
-        *reinterpret_cast<uint16_t*>(row + NB * c + 2 * bp) = uint16_t(a0 | (a1 << 4) | (b0 << 8) | (b1 << 12));
-      if (c == 0)
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const int c = (V * j + i) / 2;
+        if constexpr (KIND == KV_Q8_0)
+          *reinterpret_cast<uint32_t*>(row + 2 * NB * c + 4 * bp) = a[i] | (a[i + 1] << 8) | (b[i] << 16) | (b[i + 1] << 24);
+        else
+          *reinterpret_cast<uint16_t*>(row + NB * c + 2 * bp) = uint16_t(a[i] | (a[i + 1] << 4) | (b[i] << 8) | (b[i + 1] << 12));
+      }
+      if (j == 0)
         *reinterpret_cast<uint32_t*>(chunk + kv_scales_at(KIND, D, shift, tok) + 4 * bp) = s0 | (s1 << 16);
     }
   }
 }
 
-// The decoder's lane (j, bp) takes a 16-byte unit of the output in each of
-// blocks 2 bp and 2 bp + 1: elements V j .. V j + V - 1, from V / 2 columns.
-template <class T, int D>
-struct UnitShape {
-  static constexpr int kBlock = 32 / Elem<T>::kVec;  // lanes of a block
-  static constexpr int kLanes = kBlock * (D / 64);   // of a row
-  static constexpr int kRows = kThreads / kLanes;    // rows of a pass
-};
 template <class T, int KIND, int D>
 __device__ inline void get_units(const uint8_t* chunk, uint32_t shift, uint32_t tok, int j, int bp,
                                  float (&x)[Elem<T>::kVec], float (&y)[Elem<T>::kVec]) {
@@ -336,30 +339,31 @@ __device__ inline void get_units(const uint8_t* chunk, uint32_t shift, uint32_t 
   }
 }
 
-// Keys (blockIdx.y == 0) or values into the cache.
+// Keys (blockIdx.y == 0) or values into the cache.  Bound by the rounding's
+// instructions, about 40 an element pair: 512 tokens of 32 heads of 128 from
+// binary32 to q4_0 (43 MB with their load) 12.2 us for store and load; with an
+// element pair a lane, whose share of reductions and addresses is twice as
+// large, 13.6.
 template <class T, int KIND, int D>
 __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvView cache, Rows k, Rows v, const int64_t* slots,
-                                                            int64_t rows) {
-  constexpr int L = PairShape<D>::kLanes;
+                                                            uint32_t rows) {
+  constexpr int V = Elem<T>::kVec;
+  using S = UnitShape<V, D>;
   const Rows in = blockIdx.y ? v : k;
   uint8_t* buf = blockIdx.y ? cache.v : cache.k;
-  const int lane = threadIdx.x % L, c = lane & 15, bp = lane >> 4;
-  const int64_t r = int64_t(blockIdx.x) * PairShape<D>::kRows + threadIdx.x / L;
-  f32x2 x{0.f, 0.f}, y{0.f, 0.f};
-  int64_t slot = -1;
-  uint32_t head = 0;
-  if (r < rows) {
-    const uint32_t tok = uint32_t(r / cache.heads);
-    head = uint32_t(r - int64_t(tok) * cache.heads);
-    const uint8_t* src = in.p + tok * in.ld + (int64_t(head) * D + 64 * bp + 2 * c) * int(sizeof(T));
-    x = Elem<T>::pair(src);
-    y = Elem<T>::pair(src + 32 * sizeof(T));
-    slot = slots[tok];
-  }
+  const int lane = threadIdx.x % S::kLanes, j = lane % S::kBlock, bp = lane / S::kBlock;
+  const uint32_t r = blockIdx.x * S::kRows + threadIdx.x / S::kLanes;
+  if (r >= rows) return;
+  const uint32_t tok = r / cache.heads, head = r - tok * cache.heads;
+  const u32x4* src = reinterpret_cast<const u32x4*>(in.p + tok * in.ld + (int64_t(head) * D + 64 * bp) * int(sizeof(T))) + j;
+  float x[V], y[V];
+  Elem<T>::unpack(src[0], x);
+  Elem<T>::unpack(src[S::kBlock], y);
+  const int64_t slot = slots[tok];
   const bool in_cache = kv_slot_in(cache, slot);
   const int64_t s = in_cache ? slot : 0;
-  put_row<KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
-                   uint32_t(s & ((int64_t(1) << cache.shift) - 1)), c, bp, x, y, in_cache);
+  put_units<KIND, D, V>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
+                        uint32_t(s & ((int64_t(1) << cache.shift) - 1)), j, bp, x, y, in_cache);
 }
 
 // The cache's keys (blockIdx.y == 0) or values as rows.  Bound by the bytes
@@ -368,15 +372,15 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvView cache, Rows k
 // two blocks, 4-byte stores) took 34.2 and stores past the caches 27.
 template <class T, int KIND, int D>
 __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvView cache, Rows k, Rows v, const int64_t* slots,
-                                                           int64_t rows) {
-  using S = UnitShape<T, D>;
+                                                           uint32_t rows) {
+  using S = UnitShape<Elem<T>::kVec, D>;
   const Rows out = blockIdx.y ? v : k;
   const uint8_t* buf = blockIdx.y ? cache.v : cache.k;
   const int lane = threadIdx.x % S::kLanes, j = lane % S::kBlock, bp = lane / S::kBlock;
-  const int64_t r = int64_t(blockIdx.x) * S::kRows + threadIdx.x / S::kLanes;
+  const uint32_t r = blockIdx.x * S::kRows + threadIdx.x / S::kLanes;
   if (r >= rows) return;
   float x[Elem<T>::kVec] = {}, y[Elem<T>::kVec] = {};
-  const uint32_t tok = uint32_t(r / cache.heads), head = uint32_t(r - int64_t(tok) * cache.heads);
+  const uint32_t tok = r / cache.heads, head = r - tok * cache.heads;
   const int64_t s = slots[tok];
   if (kv_slot_in(cache, s))
     get_units<T, KIND, D>(buf + kv_chunk_at(cache, s >> cache.shift, head), cache.shift,
@@ -394,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void qkv_rope_store_kernel(KvView cache, 
                                                                   int hq, int rope_chunks, int chunks,
                                                                   const int64_t* slots, RopeArgs r) {
   using S = RowShape<T, D>;
-  using E = PairShape<D>;
+  constexpr int V = S::kVec;
   __shared__ f32x2 cs[D / 2];
   __shared__ __attribute__((aligned(16))) float rows_f32[S::kRows * D];
   const int64_t tok = blockIdx.x / unsigned(chunks);
@@ -405,17 +409,16 @@ __global__ __launch_bounds__(kThreads) void qkv_rope_store_kernel(KvView cache, 
   const int64_t s = in_cache ? slot : 0;
   const int64_t page = s >> cache.shift;
   const uint32_t at = uint32_t(s & ((int64_t(1) << cache.shift) - 1));
-  const int lane = threadIdx.x % E::kLanes, c = lane & 15, bp = lane >> 4;
   if (chunk >= rope_chunks) {  // uniform over the workgroup
+    using E = UnitShape<V, D>;
+    const int lane = threadIdx.x % E::kLanes, j = lane % E::kBlock, bp = lane / E::kBlock;
     const int head = (chunk - rope_chunks) * E::kRows + threadIdx.x / E::kLanes;
-    f32x2 x{0.f, 0.f}, y{0.f, 0.f};
-    if (head < hk) {
-      const uint8_t* src = v.p + tok * v.ld + (int64_t(head) * D + 64 * bp + 2 * c) * int(sizeof(T));
-      x = Elem<T>::pair(src);
-      y = Elem<T>::pair(src + 32 * sizeof(T));
-    }
-    put_row<KIND, D>(cache.v + kv_chunk_at(cache, page, head < hk ? head : 0), cache.shift, at, c, bp, x, y,
-                     in_cache && head < hk);
+    if (head >= hk) return;
+    const u32x4* src = reinterpret_cast<const u32x4*>(v.p + tok * v.ld + (int64_t(head) * D + 64 * bp) * int(sizeof(T))) + j;
+    float x[V], y[V];
+    Elem<T>::unpack(src[0], x);
+    Elem<T>::unpack(src[E::kBlock], y);
+    put_units<KIND, D, V>(cache.v + kv_chunk_at(cache, page, head), cache.shift, at, j, bp, x, y, in_cache);
     return;
   }
   const int first = chunk * S::kRows, row = first + threadIdx.x / S::kLanes, l = threadIdx.x % S::kLanes;
@@ -449,16 +452,16 @@ __global__ __launch_bounds__(kThreads) void qkv_rope_store_kernel(KvView cache, 
   }
   if (first + S::kRows <= hq) return;  // no key row here (uniform)
   __syncthreads();
+  using E = UnitShape<4, D>;
+  const int lane = threadIdx.x % E::kLanes, j = lane % E::kBlock, bp = lane / E::kBlock;
   for (int i = threadIdx.x / E::kLanes; i < S::kRows; i += E::kRows) {
     const int head = first + i - hq;
-    const bool here = head >= 0 && head < hk;
-    f32x2 x{0.f, 0.f}, y{0.f, 0.f};
-    if (here) {
-      x = *reinterpret_cast<const f32x2*>(rows_f32 + i * D + 64 * bp + 2 * c);
-      y = *reinterpret_cast<const f32x2*>(rows_f32 + i * D + 64 * bp + 32 + 2 * c);
-    }
-    put_row<KIND, D>(cache.k + kv_chunk_at(cache, page, here ? head : 0), cache.shift, at, c, bp, x, y,
-                     in_cache && here);
+    if (head < 0 || head >= hk) continue;
+    const u32x4* src = reinterpret_cast<const u32x4*>(rows_f32 + i * D + 64 * bp) + j;
+    float x[4], y[4];
+    Elem<float>::unpack(src[0], x);
+    Elem<float>::unpack(src[E::kBlock], y);
+    put_units<KIND, D, 4>(cache.k + kv_chunk_at(cache, page, head), cache.shift, at, j, bp, x, y, in_cache);
   }
 }
 
@@ -515,10 +518,10 @@ hipError_t launch_kv_store(const KvView& c, int kind, int D, skg_dtype dt, int64
   return by_type(dt, [&](auto t) {
     return by_dim(D, [&](auto d) {
       return by_kind(kind, [&](auto kd) {
-        const int64_t rows = T * c.heads, grid = (rows + PairShape<d()>::kRows - 1) / PairShape<d()>::kRows;
-        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        const int64_t rows = T * c.heads, grid = (rows + UnitShape<Elem<decltype(t)>::kVec, d()>::kRows - 1) / UnitShape<Elem<decltype(t)>::kVec, d()>::kRows;
+        if (rows > INT32_MAX) return hipErrorInvalidValue;
         hipLaunchKernelGGL((kv_store_kernel<decltype(t), kd(), d()>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
-                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, rows);
+                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, uint32_t(rows));
         return hipGetLastError();
       });
     });
@@ -530,10 +533,10 @@ hipError_t launch_kv_load(const KvView& c, int kind, int D, skg_dtype dt, int64_
   return by_type(dt, [&](auto t) {
     return by_dim(D, [&](auto d) {
       return by_kind(kind, [&](auto kd) {
-        const int64_t rows = T * c.heads, grid = (rows + UnitShape<decltype(t), d()>::kRows - 1) / UnitShape<decltype(t), d()>::kRows;
-        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        const int64_t rows = T * c.heads, grid = (rows + UnitShape<Elem<decltype(t)>::kVec, d()>::kRows - 1) / UnitShape<Elem<decltype(t)>::kVec, d()>::kRows;
+        if (rows > INT32_MAX) return hipErrorInvalidValue;
         hipLaunchKernelGGL((kv_load_kernel<decltype(t), kd(), d()>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
-                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, rows);
+                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, uint32_t(rows));
         return hipGetLastError();
       });
     });
@@ -548,7 +551,7 @@ hipError_t launch_qkv_rope_store(const KvView& c, int kind, int D, skg_dtype dt,
     return by_dim(D, [&](auto d) {
       return by_kind(kind, [&](auto kd) {
         using E = decltype(t);
-        constexpr int N = RowShape<E, d()>::kRows, M = PairShape<d()>::kRows;
+        constexpr int N = RowShape<E, d()>::kRows, M = UnitShape<Elem<E>::kVec, d()>::kRows;
         const int64_t rope_chunks = (hq + int(c.heads) + N - 1) / N, chunks = rope_chunks + (c.heads + M - 1) / M;
         if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
         hipLaunchKernelGGL((qkv_rope_store_kernel<E, kd(), d()>), dim3(unsigned(T * chunks)), dim3(kThreads), 0,
