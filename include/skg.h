@@ -356,8 +356,9 @@ typedef struct skg_rope {
  * apart, of hq / hk heads of head_dim), qo and ko the results in the same type,
  * rounded once.  hq or hk may be 0 (then its pointers are not read).  q == qo
  * with ldq == ldqo (and k likewise) works in place; any other overlap of an
- * input with an output, or of the outputs, is refused.  Row pointers are 16-byte aligned and row
- * strides a multiple of 16 bytes, at least heads * head_dim elements (T > 1).
+ * input with an output, or of the outputs, is refused.  Row pointers are
+ * 16-byte aligned and row strides a multiple of 16 bytes, at least heads *
+ * head_dim elements (T > 1).
  * 1 <= T <= 2^24; head_dim 64, 128 or 256; hq + hk in 1..65535.
  * Errors: SKG_E_SHAPE (T, heads, head_dim, rot, strides), SKG_E_INVALID_ARG
  * (null pointers, unknown dtype, eps, overlaps), SKG_E_ALIGN.
@@ -437,7 +438,7 @@ skg_status skg_qkv_rope_store(const skg_kv_cache* cache, skg_dtype dtype, int64_
  * Products of a key and a query, probabilities and sums keep binary32's
  * precision for SKG_F32 (terms of 11 or 8 bits each on the matrix cores) and one
  * fp16 or bf16 rounding of q and p for SKG_BF16; sums are binary32.  The result
- * does not change from call to call.  q, o and oq do not overlap.
+ * does not change from call to call.  o, oq and ws overlap nothing else.
  *
  * T >= 1, n_seqs 1..65535, 1 <= max_draft <= 64, width 1..2^26, scale finite;
  * hq a multiple of the cache's heads, hq / heads <= 256; T <= 2^24.

@@ -95,9 +95,13 @@ bool overlap(const Span& a, const Span& b, int64_t T, skg_dtype dt) {
   return d < first || d + second > period;
 }
 
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + nb && pb < pa + na;
+}
+
 bool overlap_bytes(const Span& a, int64_t T, skg_dtype dt, const void* p, size_t n) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(p);
-  return pa < pb + n && pb < pa + uintptr_t(((T - 1) * a.ld + a.width) * elem_bytes(dt));
+  return meet(a.p, size_t((T - 1) * a.ld + a.width) * size_t(elem_bytes(dt)), p, n);
 }
 
 skg_status check_rope(const skg_rope* r, int D) {
@@ -127,7 +131,6 @@ skg_status check_in_out(const Span& in, const Span& out, int64_t T, skg_dtype dt
   } while (0)
 
 skg_status launched(hipError_t e, const char* what) {
-  if (e == hipErrorInvalidValue) return fail(SKG_E_SHAPE, "%s: more rows than one launch takes", what);
   if (e != hipSuccess) return fail(SKG_E_HIP, "%s: %s", what, hipGetErrorString(e));
   return ok();
 }
@@ -303,12 +306,17 @@ skg_status skg_tree_attn(const skg_kv_cache* cache, skg_dtype dtype, int64_t T, 
     if (!aligned(oq, 4)) return fail(SKG_E_ALIGN, "oq must be 4-byte aligned");
     if (overlap_bytes(sq, T, dtype, oq, nq) || (o && overlap_bytes(so, T, dtype, oq, nq)))
       return fail(SKG_E_INVALID_ARG, "oq overlaps q or o");
+    if (meet(oq, nq, cache->k, bytes) || meet(oq, nq, cache->v, bytes))
+      return fail(SKG_E_INVALID_ARG, "oq overlaps the cache");
   }
   const size_t need = tree_attn_workspace(cache->fmt, cache->head_dim, cache->heads, dtype, T, n_seqs, hq, max_draft, max_kv);
   if (need) {
     if (!ws || ws_bytes < need)
       return fail(SKG_E_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, ws ? ws_bytes : size_t(0));
     if (!aligned(ws, 256)) return fail(SKG_E_ALIGN, "ws must be 256-byte aligned");
+    if (meet(ws, need, cache->k, bytes) || meet(ws, need, cache->v, bytes) || overlap_bytes(sq, T, dtype, ws, need) ||
+        (o && overlap_bytes(so, T, dtype, ws, need)) || (oq && meet(ws, need, oq, size_t(T) * size_t(w / QK) * 36)))
+      return fail(SKG_E_INVALID_ARG, "ws overlaps another argument");
   }
   SKG_TRY(check_device());
   const int es = elem_bytes(dtype);

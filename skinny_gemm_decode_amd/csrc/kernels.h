@@ -30,7 +30,7 @@ hipError_t launch_gemm_tiled(int64_t M, int64_t K, int64_t N, const void* W, con
                              float* y, hipStream_t stream);
 
 // Rotation, cache and attention.  Counts, strides (elements) and pointers are
-// checked by the ABI; hipErrorInvalidValue means more rows than a grid takes.
+// checked by the ABI.
 hipError_t launch_qk_norm_rope(skg_dtype dt, int64_t T, int hq, int hk, int D, const void* q, int64_t ldq,
                                const void* k, int64_t ldk, const skg_rope* rope, void* qo, int64_t ldqo, void* ko,
                                int64_t ldko, hipStream_t stream);

@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kManyGroups = 1024;  // four workgroups a CU
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;  // of a launch, which has less than 2^32 threads
 
 template <int CTRL>
 __device__ inline int dpp_u(int v) {
@@ -465,12 +466,26 @@ __global__ __launch_bounds__(kThreads) void qkv_rope_store_kernel(KvView cache, 
   }
 }
 
-RopeArgs rope_args(const skg_rope* r) {
-  return RopeArgs{r->rot, r->interleaved, r->norm, r->eps, r->pos, r->inv_freq, r->gq, r->gk};
+// The arguments of a launch that begins at token t.
+RopeArgs rope_args(const skg_rope* r, int64_t t) {
+  return RopeArgs{r->rot, r->interleaved, r->norm, r->eps, r->pos ? r->pos + t : nullptr, r->inv_freq, r->gq, r->gk};
 }
 
-Rows rows_of(const void* p, int64_t ld, skg_dtype dt) {
-  return Rows{static_cast<uint8_t*>(const_cast<void*>(p)), ld * (dt == SKG_F32 ? 4 : 2)};
+Rows rows_of(const void* p, int64_t ld, skg_dtype dt, int64_t t) {
+  const int64_t bytes = ld * (dt == SKG_F32 ? 4 : 2);
+  return Rows{p ? static_cast<uint8_t*>(const_cast<void*>(p)) + t * bytes : nullptr, bytes};
+}
+
+// f(t, n) for tokens t .. t + n - 1, in as few launches as they fit: `groups`
+// workgroups for `tokens` of them.
+template <class F>
+hipError_t by_tokens(int64_t T, int64_t tokens, int64_t groups, F&& f) {
+  const int64_t most = kMaxGroups / groups * tokens;
+  for (int64_t t = 0; t < T; t += most) {
+    f(t, T - t < most ? T - t : most);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Calls f with the type, cache kind and head size as template arguments.
@@ -501,11 +516,11 @@ hipError_t launch_qk_norm_rope(skg_dtype dt, int64_t T, int hq, int hk, int D, c
       constexpr int N = RowShape<E, d()>::kRows;
       auto launch = [&](auto kernel, int rows) {  // rows of a workgroup
         const int64_t chunks = (hq + hk + rows - 1) / rows;
-        if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(kernel, dim3(unsigned(T * chunks)), dim3(kThreads), 0, stream, rows_of(q, ldq, dt),
-                           rows_of(k, ldk, dt), rows_of(qo, ldqo, dt), rows_of(ko, ldko, dt), hq, hk, int(chunks),
-                           rope_args(rope));
-        return hipGetLastError();
+        return by_tokens(T, 1, chunks, [&](int64_t t, int64_t n) {
+          hipLaunchKernelGGL(kernel, dim3(unsigned(n * chunks)), dim3(kThreads), 0, stream, rows_of(q, ldq, dt, t),
+                             rows_of(k, ldk, dt, t), rows_of(qo, ldqo, dt, t), rows_of(ko, ldko, dt, t), hq, hk,
+                             int(chunks), rope_args(rope, t));
+        });
       };
       if (T * ((hq + hk + N - 1) / N) >= kManyGroups) return launch(qk_norm_rope_kernel<E, d(), 2>, 2 * N);
       return launch(qk_norm_rope_kernel<E, d(), 1>, N);
@@ -518,11 +533,13 @@ hipError_t launch_kv_store(const KvView& c, int kind, int D, skg_dtype dt, int64
   return by_type(dt, [&](auto t) {
     return by_dim(D, [&](auto d) {
       return by_kind(kind, [&](auto kd) {
-        const int64_t rows = T * c.heads, grid = (rows + UnitShape<Elem<decltype(t)>::kVec, d()>::kRows - 1) / UnitShape<Elem<decltype(t)>::kVec, d()>::kRows;
-        if (rows > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((kv_store_kernel<decltype(t), kd(), d()>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
-                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, uint32_t(rows));
-        return hipGetLastError();
+        constexpr int N = UnitShape<Elem<decltype(t)>::kVec, d()>::kRows;
+        return by_tokens(T, N, c.heads, [&](int64_t t0, int64_t n) {  // N tokens fill as many workgroups as they have heads
+          const int64_t rows = n * c.heads;
+          hipLaunchKernelGGL((kv_store_kernel<decltype(t), kd(), d()>), dim3(unsigned((rows + N - 1) / N), 2),
+                             dim3(kThreads), 0, stream, c, rows_of(k, ldk, dt, t0), rows_of(v, ldv, dt, t0), slots + t0,
+                             uint32_t(rows));
+        });
       });
     });
   });
@@ -533,11 +550,13 @@ hipError_t launch_kv_load(const KvView& c, int kind, int D, skg_dtype dt, int64_
   return by_type(dt, [&](auto t) {
     return by_dim(D, [&](auto d) {
       return by_kind(kind, [&](auto kd) {
-        const int64_t rows = T * c.heads, grid = (rows + UnitShape<Elem<decltype(t)>::kVec, d()>::kRows - 1) / UnitShape<Elem<decltype(t)>::kVec, d()>::kRows;
-        if (rows > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((kv_load_kernel<decltype(t), kd(), d()>), dim3(unsigned(grid), 2), dim3(kThreads), 0,
-                           stream, c, rows_of(k, ldk, dt), rows_of(v, ldv, dt), slots, uint32_t(rows));
-        return hipGetLastError();
+        constexpr int N = UnitShape<Elem<decltype(t)>::kVec, d()>::kRows;
+        return by_tokens(T, N, c.heads, [&](int64_t t0, int64_t n) {  // N tokens fill as many workgroups as they have heads
+          const int64_t rows = n * c.heads;
+          hipLaunchKernelGGL((kv_load_kernel<decltype(t), kd(), d()>), dim3(unsigned((rows + N - 1) / N), 2),
+                             dim3(kThreads), 0, stream, c, rows_of(k, ldk, dt, t0), rows_of(v, ldv, dt, t0), slots + t0,
+                             uint32_t(rows));
+        });
       });
     });
   });
@@ -553,11 +572,12 @@ hipError_t launch_qkv_rope_store(const KvView& c, int kind, int D, skg_dtype dt,
         using E = decltype(t);
         constexpr int N = RowShape<E, d()>::kRows, M = UnitShape<Elem<E>::kVec, d()>::kRows;
         const int64_t rope_chunks = (hq + int(c.heads) + N - 1) / N, chunks = rope_chunks + (c.heads + M - 1) / M;
-        if (T * chunks > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((qkv_rope_store_kernel<E, kd(), d()>), dim3(unsigned(T * chunks)), dim3(kThreads), 0,
-                           stream, c, rows_of(q, ldq, dt), rows_of(k, ldk, dt), rows_of(v, ldv, dt),
-                           rows_of(qo, ldqo, dt), hq, int(rope_chunks), int(chunks), slots, rope_args(rope));
-        return hipGetLastError();
+        return by_tokens(T, 1, chunks, [&](int64_t t0, int64_t n) {
+          hipLaunchKernelGGL((qkv_rope_store_kernel<E, kd(), d()>), dim3(unsigned(n * chunks)), dim3(kThreads), 0,
+                             stream, c, rows_of(q, ldq, dt, t0), rows_of(k, ldk, dt, t0), rows_of(v, ldv, dt, t0),
+                             rows_of(qo, ldqo, dt, t0), hq, int(rope_chunks), int(chunks), slots + t0,
+                             rope_args(rope, t0));
+        });
       });
     });
   });

@@ -1041,7 +1041,7 @@ __global__ __launch_bounds__(256, (AttnShape<KIND, D, NT, RT, 4, false>::kPerCu)
   }
   // where the wave's next 32 steps lie, two tiles each, over its lanes
   const int32_t* table = a.table + int64_t(unit.seq) * a.width;
-  auto key_of = [&](int i) SKG_INL { return (unit.begin + wave + i * kWaves) * kStep; };
+  auto key_of = [&](int i) SKG_INL { return int(unsigned(unit.begin + wave + i * kWaves) * kStep); };
   auto where_from = [&](int i0) SKG_INL {
     const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
     return steps_at<KIND, D>(a.cache, head, key, i < n && key < sp.keys ? table[key >> a.cache.shift] : -1);
@@ -1222,7 +1222,7 @@ __global__ __launch_bounds__(64 * W, (W == 8 ? 2 : AttnShape<KIND, D, NT, RT, W,
     w.mask[rt] = !is ? 0 : a.mask ? a.mask[sp.t0 + i] : ~uint64_t(0) >> (63 - i);
   }
   const int32_t* table = a.table + int64_t(unit.seq) * a.width;
-  auto key_of = [&](int i) SKG_INL { return (unit.begin + i) * kStep; };
+  auto key_of = [&](int i) SKG_INL { return int(unsigned(unit.begin + i) * kStep); };
   auto where_from = [&](int i0) SKG_INL {
     const int i = i0 + (lane >> 1), key = key_of(i) + 16 * (lane & 1);
     return steps_at<KIND, D>(a.cache, head, key, i < n && key < sp.keys ? table[key >> a.cache.shift] : -1);

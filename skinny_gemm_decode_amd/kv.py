@@ -191,8 +191,9 @@ def qk_norm_rope(q, k, pos, inv_freq, gq=None, gk=None, eps: float = 1e-6, norm:
         raise ValueError("q or k is required")
     dev = _device(x, "q" if q is not None else "k")
     dt = _dtype(x, "q" if q is not None else "k")
-    if x.dim() != 3:
-        raise ValueError(f"rows must be [T, heads, head_dim] (got {list(x.shape)})")
+    for t in (q, k):
+        if t is not None and t.dim() != 3:
+            raise ValueError(f"rows must be [T, heads, head_dim] (got {list(t.shape)})")
     T, _, D = x.shape
     hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
     r = _rope(T, hq, hk, D, pos, inv_freq, gq, gk, eps, norm, interleaved, dev)
@@ -233,7 +234,9 @@ def kv_store(cache: KvCache, k, v, slots, stream=None) -> None:
     dt = _dtype(k, "k")
     if cache._device != dev:
         raise ValueError("the cache must be on the current GPU")
-    T = len(k)
+    if k.dim() != 3:
+        raise ValueError(f"rows must be [T, heads, head_dim] (got {list(k.shape)})")
+    T = k.shape[0]
     shape = (T, cache.heads, cache.head_dim)
     kp, ldk = _rows(k, "k", shape, k.dtype, dev)
     vp, ldv = _rows(v, "v", shape, k.dtype, dev)

@@ -303,3 +303,28 @@ def test_on_another_stream(skg, torch):
         y, _ = skg.qk_norm_rope(xd, None, pos, fd, stream=stream)
         s.synchronize()
         assert torch.equal(y, want)
+
+
+def test_largest_token_count(skg, torch):
+    """2^24 tokens, one more than the workgroups of a launch: rotation, store
+    and load of one head of 64, compared at the seam and at both ends."""
+    T = 1 << 24
+    note("rope, store and load of 2^24 tokens")
+    x = torch.randn((T, 1, 64), device="cuda", dtype=torch.bfloat16, generator=torch.Generator("cuda").manual_seed(3))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    f = freqs(64)
+    at = np.array([0, 1, 77777, T - 3, T - 2, T - 1])
+    rows = host(x[at].float())
+    o, _ = skg.qk_norm_rope(x, None, pos, dev(f))
+    ref = oracle.rope_ref(rows, at, f, False)
+    assert np.all(np.abs(host(o[at].float()) - ref) <= 2.0**-8 * np.abs(ref) + 2.0**-20)
+    del o
+    page = 1 << 12
+    c = skg.kv_cache(skg.KV_Q8_0, 1, 64, page, T // page)
+    slots = torch.arange(T, device="cuda").flip(0)
+    skg.kv_store(c, x, x, slots)
+    k, v = skg.kv_load(c, slots, dtype=torch.bfloat16)
+    want = oracle.kv_decode("q8_0", *oracle.kv_encode("q8_0", rows))
+    for t in (k, v):
+        assert np.all(np.abs(host(t[at].float()) - want) <= 2.0**-8 * np.abs(want))
+    assert bool((k == v).all())

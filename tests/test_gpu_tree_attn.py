@@ -400,3 +400,27 @@ def test_float32_rows_keep_float32_scores(skg, torch, fmt, D, n):
     p = Problem(skg, torch, fmt, [1 if n == 1 else 3], [n], 64, 64 if n == 1 else 8, D, 16, masks=None, qs=2.0, seed=5)
     o, want = p.run().astype(np.float64), p.reference()[0]
     assert np.sqrt(np.mean((o - want) ** 2)) <= 2.0**-20
+
+
+@pytest.mark.parametrize("fmt", oracle.KV_FMTS)
+def test_pages_past_32_bit_offsets(skg, torch, fmt):
+    """A cache buffer over 4 GiB: keys on its last pages, against the same keys
+    in a small cache (the order of pages is not seen)."""
+    H, D, page, n = 32, 128, 64, 200
+    per = skg.kv_bytes(kinds(skg)[fmt], H, D, page, 1)
+    pages = (1 << 32) // per + 9
+    note(f"tree_attn and store past 4 GiB {fmt}: {pages} pages")
+    rng = np.random.default_rng(8)
+    k, v, q = (dev(values(rng, (m, H, D))) for m in (n, n, 3))
+    out = []
+    for total, table in ((pages, [pages - 1, pages - 3, pages - 2, pages - 5]), (4, [0, 2, 1, 3])):
+        c = skg.kv_cache(kinds(skg)[fmt], H, D, page, total)
+        t = torch.tensor([table], dtype=torch.int32, device="cuda")
+        j = torch.arange(n, device="cuda")
+        slots = t[0].long()[j // page] * page + j % page
+        skg.kv_store(c, k, v, slots)
+        out.append((skg.tree_attn(c, q, t, dev(np.array([n - 3], np.int32))), *skg.kv_load(c, slots)))
+        del c
+    for a, b in zip(*out):
+        assert np.array_equal(host(a), host(b))
+    assert np.all(np.isfinite(host(out[0][0]))) and np.abs(host(out[0][0])).max() > 0

@@ -156,6 +156,10 @@ def test_tree_attn_refusals(skg):
     assert call(ws=ptr(60), wsb=size - 1, **long) == skg.E_INVALID_ARG
     assert call(ws=None, wsb=size, **long) == skg.E_INVALID_ARG
     assert call(ws=ptr(60, 128), wsb=size, **long) == skg.E_ALIGN
+    # workspace or Q8_1 blocks over another argument
+    for kw in (dict(ws=ptr(0)), dict(ws=ptr(10)), dict(ws=ptr(800)), dict(ws=ptr(2000)), dict(ws=ptr(20), oq=ptr(20, 64))):
+        assert call(wsb=size, **{**long, **kw}) == skg.E_INVALID_ARG, kw
+    assert call(o=None, oq=ptr(800)) == skg.E_INVALID_ARG
     # the same cache with a small bound on its keys needs none
     assert skg.lib.skg_tree_attn_workspace(cache(skg, pages=1000), F32, 4, 2, 8, 2, 500, 200) == 0
 
