@@ -268,10 +268,6 @@ constexpr uint32_t kZero = 0x80808080u;  // two -128 2^-24
 __device__ inline uint32_t two_bytes(uint32_t w0, int y0, uint32_t w1, int y1) {
   return __builtin_amdgcn_perm(w1, w0, 0x0C000C00u | uint32_t((4 + y1) << 16) | uint32_t(y0));
 }
-// The low (hi = 0) or high 16 bits of w0 and w1.
-__device__ inline uint32_t two_halves(uint32_t w0, uint32_t w1, int hi) {
-  return __builtin_amdgcn_perm(w1, w0, hi ? 0x07060302u : 0x05040100u);
-}
 
 // NT terms of q and p; RT tiles of 16 rows a wave; W waves, which share the keys
 // of a split between them (each its own steps) or, with ROWS, the rows (all the
@@ -331,6 +327,13 @@ __device__ inline int k_swizzle(int c) {
 }
 // LDS row of V's key c (and back): the rows 4g + i of the four g differ modulo 4.
 __device__ inline int v_row(int c) { return c ^ (c >> 2); }
+// Offset in a tile of the 16-byte unit that a transfer puts at unit u of row c:
+// for K, and V in bf16, swizzled units; for V's codes permuted rows.
+template <class S, bool V>
+__device__ inline uint32_t tile_unit(int c, int u) {
+  if (V && S::kF16) return v_row(c) * S::kRow + 16 * u;
+  return c * S::kRow + 16 * (u ^ k_swizzle<S::kRC>(c));
+}
 
 __device__ inline void dma4(const void* src, uint32_t dst) {
 #pragma clang diagnostic push
@@ -407,7 +410,7 @@ __device__ inline void copy_step(const KvView& c, const StepAt& from, uint32_t d
 #pragma unroll
       for (int j = 0; j < S::kRow / 64; ++j) {
         const int row = j * (64 / S::kRC) + lane / S::kRC, unit = lane % S::kRC;
-        const uint32_t off = V ? v_row(row) * S::kRow + 16 * unit : row * S::kRow + 16 * (unit ^ k_swizzle<S::kRC>(row));
+        const uint32_t off = tile_unit<S, V>(row, unit);
         dma16_sv_stream(buf + from.codes[t], off, codes + t * S::kTile + 1024 * j);
       }
   } else {  // both tiles in one transfer
@@ -441,7 +444,7 @@ __device__ inline void copy_part(const KvView& c, const StepAt& from, uint32_t d
     if constexpr (S::kRow >= 64) {
       const int y = v ? x - kAll / 2 : x, t = y / (S::kRow / 64), i = y % (S::kRow / 64);
       const int row = i * (64 / S::kRC) + lane / S::kRC, unit = lane % S::kRC;
-      const uint32_t off = v ? v_row(row) * S::kRow + 16 * unit : row * S::kRow + 16 * (unit ^ k_swizzle<S::kRC>(row));
+      const uint32_t off = v ? tile_unit<S, true>(row, unit) : tile_unit<S, false>(row, unit);
       dma16_sv(buf + (t ? from.codes[1] : from.codes[0]), off, dst + (v ? S::kVOff : S::kKOff) + t * S::kTile + 1024 * i);
     } else {
       const int row = (lane & 31) / 2, unit = lane & 1;
@@ -486,7 +489,9 @@ __device__ inline void load_words(const uint8_t* p, uint32_t* w) {
 template <class S>
 struct StepRegs {
   uint32_t k[2][S::KW];   // key c of each tile, its elements 8g .. 8g + 7 of every block
-  uint32_t v[8][S::VW];   // keys 4g + i (tile 0), 4g + i - 4 (tile 1), column c
+  // codes: keys 4g + i (tile 0), 4g + i - 4 (tile 1), column c; bf16: words
+  // 4n .. 4n + 3 are element 16n + c of those keys in pairs
+  uint32_t v[8][S::VW];
   uint32_t sk[2][S::SW];  // scales of keys 4g .. 4g + 3 of each tile
   uint32_t sv[2][S::SW];
   uint32_t all[2];        // the step's scales of V, spread over the lanes
@@ -513,9 +518,34 @@ __device__ inline void read_k(StepRegs<S>& r, const uint8_t* slot) {
     if constexpr (S::kF16) load_words<S::SW>(slot + S::kSkOff + (16 * t + 4 * g) * 2 * S::NB, r.sk[t]);
   }
 }
+// Word w of StepRegs::v.
+template <class S>
+__device__ inline uint32_t& v_word(StepRegs<S>& r, int w) { return r.v[w / S::VW][w % S::VW]; }
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
 template <class S, int KIND>
 __device__ inline void read_v(StepRegs<S>& r, const uint8_t* slot) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  if constexpr (KIND == KV_BF16) {
+    // Transposing reads: the 16 lanes of g give the addresses of four elements
+    // of keys 4g .. 4g + 3 each, and get one element of all four.
+    const int row = 4 * g + (c >> 2);
+    const uint32_t at = lds_addr(slot) + S::kVOff + row * S::kRow + 8 * (c & 1);
+    const int z = k_swizzle<S::kRC>(row) ^ ((c >> 1) & 1);
+#pragma unroll
+    for (int n = 0; n < 2 * S::NB; ++n)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t from = at + 16 * ((2 * n) ^ z) + t * S::kTile;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)from);
+        const uint2 y = __builtin_bit_cast(uint2, x);
+        v_word(r, 4 * n + 2 * t) = y.x;
+        v_word(r, 4 * n + 2 * t + 1) = y.y;
+      }
+    return;
+  }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -557,15 +587,15 @@ __device__ inline u32x4 k_operand(const StepRegs<S>& r, int t, int b) {
   return a;
 }
 
-// V operand: column element n of the lane's eight keys.  Quantised: n = 2 b + e;
-// bf16: element (D / 16) c + n.
+// V operand: an element of the lane's eight keys.  Quantised: n = 2 b + e of
+// column c; bf16: element 16 n + c.
 template <class S, int KIND>
-__device__ inline u32x4 v_operand(const StepRegs<S>& r, int n) {
+__device__ inline u32x4 v_operand(StepRegs<S>& r, int n) {
   u32x4 a;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (KIND == KV_BF16) {
-      a[i] = two_halves(r.v[2 * i][n >> 1], r.v[2 * i + 1][n >> 1], n & 1);
+      a[i] = v_word(r, 4 * n + i);
     } else if constexpr (KIND == KV_Q8_0) {
       a[i] = q8_pair(two_bytes(r.v[2 * i][n >> 2], n & 3, r.v[2 * i + 1][n >> 2], n & 3));
     } else {
@@ -756,17 +786,17 @@ __device__ inline void do_values(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, floa
     if constexpr (EDGE) {
       // a value that is not there may be anything: zero; one that some rows
       // see may be infinite or NaN, which must not reach the others as 0 * v
-      uint32_t bad = 0;
+      uint32_t bad = 0, in[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = r.key + 16 * (i >> 2) + 4 * g + (i & 3);
-        const bool in = r.there[i >> 2] && key < keys;
+      for (int i = 0; i < 4; ++i) {
+        const int key = r.key + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
+        in[i] = !r.there[i >> 1] || key >= keys ? 0u : key + 1 < keys ? ~0u : 0xFFFFu;
+      }
 #pragma unroll
-        for (int j = 0; j < S::VW; ++j) {
-          const uint32_t x = in ? r.v[i][j] : 0;
-          r.v[i][j] = x;
-          bad |= uint32_t((x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u);
-        }
+      for (int j = 0; j < D / 4; ++j) {
+        const uint32_t x = v_word(r, j) & in[j & 3];
+        v_word(r, j) = x;
+        bad |= uint32_t((x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u);
       }
       if (__ballot(bad != 0)) {
         // The sums take zeros in their place; where a row sees one, which the
@@ -790,12 +820,10 @@ __device__ inline void do_values(WaveRows<S, D, NT, RT>& w, StepRegs<S>& r, floa
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < S::VW; ++j) {
-            const uint32_t x = r.v[i][j];
-            r.v[i][j] = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
-          }
+        for (int j = 0; j < D / 4; ++j) {
+          const uint32_t x = v_word(r, j);
+          v_word(r, j) = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
+        }
       }
     }
     uint32_t pt[RT][4][NT];
@@ -982,17 +1010,9 @@ __device__ inline void fill_zero(W& w) {
 template <class S, int KIND, int D>
 __device__ inline void put_tile(const f32x4 (&o)[D / 16], float (*obuf)[S::C + 4], int c, int g, int h) {
   constexpr int C = S::C;
-  if constexpr (KIND == KV_BF16) {  // element (D / 16) (4g + i) + n at [n][i]
-    constexpr int W = D / 16;
+  if constexpr (KIND == KV_BF16) {  // element 16 n + 4 g + i at [n][i]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = W * (4 * g + i);
-      if (e / C == h) {
-#pragma unroll
-        for (int m = 0; m < W; m += 4)
-          *reinterpret_cast<f32x4*>(&obuf[c][e % C + m]) = f32x4{o[m][i], o[m + 1][i], o[m + 2][i], o[m + 3][i]};
-      }
-    }
+    for (int m = 0; m < C / 16; ++m) *reinterpret_cast<f32x4*>(&obuf[c][16 * m + 4 * g]) = o[h * (C / 16) + m];
   } else {  // element 32 b + 8 g + 2 i + e at [2b + e][i]
 #pragma unroll
     for (int b = 0; b < C / 32; ++b)
