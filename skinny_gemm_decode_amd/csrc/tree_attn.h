@@ -75,19 +75,24 @@ __device__ inline KvSpan span_of(const TreeArgs& a, int b) {
   return kv_span(a.ctx[b], t0, t1, a.T, a.max_draft, a.max_kv);
 }
 
-__device__ inline int wave_sum_int(int v) {
-#pragma unroll
-  for (int i = 1; i < 64; i *= 2) v += __shfl_xor(v, i, 64);
-  return v;
+// Sum over the lanes up to each (within 16 lanes, then over the rows of 16).
+__device__ inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 to rows 1 and 3
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 to rows 2 and 3
 }
 __device__ inline int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // Splits are of equal cost over all sequences: per = the cost of all of them
 // over the splits that are wanted, so a long sequence gets many and a short one
 // gets one, and a workgroup finds its own from the lengths, one lane a sequence.
-// A step costs 1, or 2 where 256 rows share it (WEIGH) and more than half of
-// them are there (four sequences of 61, 61, 6 and 23 drafted tokens 47.9 us
-// without that, 43.4 with it; with 128 rows of three terms it cost 1.3 of 33).
+// A step costs 1; where 256 rows share it (WEIGH) 5 if more than half of them
+// are there and else 3 (four sequences of 61, 61, 6 and 23 drafted tokens 47.9
+// us without that, 43.4 with 2 and 1, 41.5 with this; steps took 1.34 and 0.8 us.
+// With 128 rows of three terms it cost 1.3 of 33).
 struct Splits {  // of 64 sequences, one a lane
   KvSpan sp;
   int n, incl;  // splits of the sequence; of it and all before it
@@ -98,13 +103,12 @@ __device__ __forceinline__ Splits lane_span(const TreeArgs& a, int b) {
   return s;
 }
 __device__ inline int steps_of(const KvSpan& sp) { return sp.keys / kStep + (sp.keys % kStep != 0); }
-template <bool WEIGH>
-__device__ inline int dear(const TreeArgs& a, const KvSpan& sp) {
-  return WEIGH && 2 * sp.n * a.group > a.tile;
-}
+constexpr int kDear = 5, kCheap = 3;
+__device__ inline bool dear(const TreeArgs& a, const KvSpan& sp) { return 2 * sp.n * a.group > a.tile; }
 template <bool WEIGH>
 __device__ inline int cost_of(const TreeArgs& a, const KvSpan& sp) {
-  return sp.n == 0 ? 0 : ((steps_of(sp) << dear<WEIGH>(a, sp)) + (1 << a.cost_shift) - 1) >> a.cost_shift;
+  const int each = !WEIGH ? 1 : dear(a, sp) ? kDear : kCheap;
+  return sp.n == 0 ? 0 : (unsigned(steps_of(sp) * each) + (1u << a.cost_shift) - 1) >> a.cost_shift;
 }
 // Cost of a split.
 template <bool WEIGH>
@@ -113,7 +117,7 @@ __device__ __forceinline__ int split_cost(const TreeArgs& a, const Splits& first
   if (a.n_seqs > 1) {
 #pragma unroll 1
     for (int b = 64; b < a.n_seqs; b += 64) total += cost_of<WEIGH>(a, lane_span(a, b + (threadIdx.x & 63)).sp);
-    total = wave_sum_int(total);
+    total = lane_of(wave_scan(total), 63);
   }
   total = __builtin_amdgcn_readfirstlane(total);
   return total / a.want + (total % a.want != 0);
@@ -121,22 +125,15 @@ __device__ __forceinline__ int split_cost(const TreeArgs& a, const Splits& first
 // Steps of a split of a sequence.
 template <bool WEIGH>
 __device__ __forceinline__ int split_steps(const TreeArgs& a, const KvSpan& sp, int cost) {
-  const int d = dear<WEIGH>(a, sp), most = (1 << 27) >> a.cost_shift;
-  const int per = (((cost < most ? cost : most) << a.cost_shift) + d) >> d;
+  const unsigned most = (1u << 27) >> a.cost_shift, c = (unsigned(cost) < most ? unsigned(cost) : most) << a.cost_shift;
+  const int per = int(!WEIGH ? c : dear(a, sp) ? (c + kDear - 1) / kDear : (c + kCheap - 1) / kCheap);
   return per < kMinSteps ? kMinSteps : per;
 }
 template <bool WEIGH>
 __device__ __forceinline__ void count_splits(const TreeArgs& a, Splits& s, int cost, int before) {
   const int per = split_steps<WEIGH>(a, s.sp, cost), n = (steps_of(s.sp) + per - 1) / per;
   s.n = s.sp.n == 0 ? 0 : n < 1 ? 1 : n;
-  int incl = s.n;
-  if (a.n_seqs > 1) {
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) {
-      const int x = __shfl_up(incl, i, 64);
-      if (int(threadIdx.x & 63) >= i) incl += x;
-    }
-  }
+  const int incl = a.n_seqs > 1 ? wave_scan(s.n) : s.n;
   s.incl = before + incl;
 }
 
