@@ -89,10 +89,10 @@ __device__ inline int lane_of(int v, int lane) { return __builtin_amdgcn_readlan
 // Splits are of equal cost over all sequences: per = the cost of all of them
 // over the splits that are wanted, so a long sequence gets many and a short one
 // gets one, and a workgroup finds its own from the lengths, one lane a sequence.
-// A step costs 1; where 256 rows share it (WEIGH) 5 if more than half of them
-// are there and else 3 (four sequences of 61, 61, 6 and 23 drafted tokens 47.9
-// us without that, 43.4 with 2 and 1, 41.5 with this; steps took 1.34 and 0.8 us.
-// With 128 rows of three terms it cost 1.3 of 33).
+// A step costs 1; where eight waves share its rows (WEIGH) 5 if more than half
+// of them are there and else 3 (trees of 61, 61, 6 and 23 drafted tokens over
+// bf16, steps of 1.34 and 0.8 us: 47.9 us without that, 41.5 with it; six of up
+// to 30 of float32 rows over q8_0 48.3 and 42.2).
 struct Splits {  // of 64 sequences, one a lane
   KvSpan sp;
   int n, incl;  // splits of the sequence; of it and all before it
@@ -1220,7 +1220,7 @@ __global__ __launch_bounds__(64 * W, (W == 8 ? 2 : AttnShape<KIND, D, NT, RT, W,
   const int c = lane & 15, g = lane >> 4;
 
   Unit unit;
-  if (!find_unit<RT * W == 16>(a, blockIdx.y, unit)) return;
+  if (!find_unit<W == 8>(a, blockIdx.y, unit)) return;
   const KvSpan sp = unit.sp;
   const int rows = sp.n * a.group, group_first = rg * 16 * RT * W;
   if (group_first >= rows) return;

@@ -108,7 +108,7 @@ hipError_t join(const TreeArgs& a, float unit, bool wide, hipStream_t stream) {
                        dim3(256), 0, stream, a, unit);
     return hipGetLastError();
   };
-  if (a.tile > 128)
+  if (a.tile > 64)
     return wide ? launch(tree_attn_join_kernel<T, D, 16, true>, 1) : launch(tree_attn_join_kernel<T, D, 4, true>, 4);
   return wide ? launch(tree_attn_join_kernel<T, D, 16, false>, 1) : launch(tree_attn_join_kernel<T, D, 4, false>, 4);
 }
