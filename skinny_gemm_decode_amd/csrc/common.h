@@ -264,15 +264,6 @@ __device__ inline void dma16_stream(const void* src, uint32_t dst) {
                "v"(src)
                : "memory", "m0");
 }
-// dma16_sv with the hint.
-__device__ inline void dma16_sv_stream(const void* base, uint32_t off, uint32_t dst) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint64_t sb = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b)))) |
-                      (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32)))) << 32);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
-               "v"(off), "s"(sb)
-               : "memory", "m0");
-}
 #pragma clang diagnostic pop
 
 // s_waitcnt vmcnt(N) (N <= 63), other counters untouched.

@@ -332,14 +332,23 @@ __device__ inline uint32_t tile_unit(int c, int u) {
   return c * S::kRow + 16 * (u ^ k_swizzle<S::kRC>(c));
 }
 
-__device__ inline void dma4(const void* src, uint32_t dst) {
+// Transfers as dma16_sv: 4 bytes a lane, and 16 with the streaming hint.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
+__device__ inline void dma4(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
                "v"(src)
                : "memory", "m0");
-#pragma clang diagnostic pop
 }
+__device__ inline void dma16_sv_stream(const void* base, uint32_t off, uint32_t dst) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t sb = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b)))) |
+                      (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32)))) << 32);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+               "v"(off), "s"(sb)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
 template <int N>
 __device__ inline void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");

@@ -33,6 +33,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 GEMV_SOURCES = ["csrc/common.h", "csrc/gemv_impl.h", "csrc/gemv_instances.h", "csrc/gemv_bf16.hip"]
 
 
+def kernel_name(name: str) -> str:
+    """A kernel without its arguments and unnamed namespaces."""
+    return name.replace("(anonymous namespace)::", "").split("(")[0]
+
+
 def gemv_source_hash() -> str:
     h = hashlib.sha256()
     for rel in GEMV_SOURCES:
@@ -48,7 +53,7 @@ def counters(dirs):
             acc = collections.defaultdict(list)
             with open(f) as fh:
                 for r in csv.DictReader(fh):
-                    acc[(r["Kernel_Name"].split("(")[0], r["Counter_Name"])].append(float(r["Counter_Value"]))
+                    acc[(kernel_name(r["Kernel_Name"]), r["Counter_Name"])].append(float(r["Counter_Value"]))
             out.append(f"== {f}")
             for (k, c), v in sorted(acc.items(), key=lambda kv: -len(kv[1])):
                 out.append(f"{c:12s} n={len(v):6d} mean={sum(v) / len(v):14.1f} min={min(v):14.1f} "
@@ -74,7 +79,7 @@ def _counter_means(d, counter):
         with open(f) as fh:
             for r in csv.DictReader(fh):
                 if r["Counter_Name"] == counter:
-                    acc[r["Kernel_Name"].split("(")[0]].append(float(r["Counter_Value"]))
+                    acc[kernel_name(r["Kernel_Name"])].append(float(r["Counter_Value"]))
     return {k: (len(v), sum(v) / len(v), max(v)) for k, v in acc.items()}
 
 
@@ -134,7 +139,7 @@ def trace_md(d, title, command):
     for f in sorted(glob.glob(os.path.join(d, "**", "*kernel_stats.csv"), recursive=True)):
         with open(f) as fh:
             for r in csv.DictReader(fh):
-                name = r["Name"].split("(")[0]
+                name = kernel_name(r["Name"])
                 if "skg::" not in name:
                     continue
                 rows.append((name, int(r["Calls"]), float(r["AverageNs"]) / 1e3, float(r["MinNs"]) / 1e3,
@@ -155,7 +160,7 @@ def counters_md(title, command, dirs):
             acc = collections.defaultdict(list)
             with open(f) as fh:
                 for r in csv.DictReader(fh):
-                    k = r["Kernel_Name"].split("(")[0]
+                    k = kernel_name(r["Kernel_Name"])
                     if "skg::" in k:
                         acc[(k, r["Counter_Name"])].append(float(r["Counter_Value"]))
             for (k, c), v in acc.items():
