@@ -424,3 +424,19 @@ def test_pages_past_32_bit_offsets(skg, torch, fmt):
     for a, b in zip(*out):
         assert np.array_equal(host(a), host(b))
     assert np.all(np.isfinite(host(out[0][0]))) and np.abs(host(out[0][0])).max() > 0
+
+
+@pytest.mark.parametrize("fmt,bf16,hq,hk,B,draft", [("q8_0", False, 2, 2, 70, 1), ("q4_0", True, 4, 1, 130, 1),
+                                                   ("q8_0", False, 4, 1, 70, 20), ("bf16", True, 8, 2, 66, 40),
+                                                   ("q4_0", False, 2, 1, 300, 2)])
+def test_many_sequences(skg, torch, fmt, bf16, hq, hk, B, draft):
+    """More sequences than a wave has lanes, long ones among them that are
+    split (up to 256 sequences; beyond that none is), at the seams of 64."""
+    note(f"tree_attn of {B} sequences {fmt} bf16={bf16} {hq}/{hk} draft={draft}")
+    rng = np.random.default_rng(B + draft)
+    ctx = [int(c) for c in rng.integers(0, 12, B)]
+    for b in (0, 62, 63, 64, B - 1):
+        ctx[b] = int(rng.integers(500, 900))
+    n = [int(t) for t in rng.integers(0, draft + 1, B)]
+    n[63], n[64], n[B - 1] = draft, 1, draft
+    Problem(skg, torch, fmt, ctx, n, hq, hk, 64, 16, bf16, seed=draft).check()
