@@ -75,4 +75,34 @@ SKG_HD inline KvSpan kv_span(int32_t ctx, int32_t t0, int32_t t1, int64_t T, int
   return s;
 }
 
+// How attention's keys are split, in steps of 32: splits of equal cost over
+// `want` of them, a sequence's cost being steps * each (its weight, 1 to 5) in
+// units of 2^shift, so that the sum over all sequences fits 31 bits.  A
+// sequence with tokens has at least one split, so all of them have at most
+// want + n_seqs: the workspace's size rests on that.
+constexpr int kStep = 32;
+constexpr int kMinSteps = 8;  // of a split at least, where a sequence is split
+constexpr int kMaxWeight = 5;
+
+SKG_HD inline int kv_cost_shift(int64_t max_kv, int n_seqs) {
+  int shift = 0;
+  while (((((max_kv + kStep - 1) / kStep * kMaxWeight) >> shift) + 1) > INT32_MAX / n_seqs) ++shift;
+  return shift;
+}
+SKG_HD inline int kv_steps(int32_t keys) { return keys / kStep + (keys % kStep != 0); }
+SKG_HD inline int kv_cost(int steps, int each, int shift) {
+  return int((uint32_t(steps) * uint32_t(each) + (1u << shift) - 1) >> shift);
+}
+// Steps of a split that costs `cost`.  A sequence has at most 2^26, so a split
+// of 2^29 / kMaxWeight always holds one whole.
+SKG_HD inline int kv_split_steps(int cost, int each, int shift) {
+  const uint32_t most = (1u << 29) >> shift, c = (uint32_t(cost) < most ? uint32_t(cost) : most) << shift;
+  const int per = int((c + uint32_t(each) - 1) / uint32_t(each));
+  return per < kMinSteps ? kMinSteps : per;
+}
+SKG_HD inline int kv_splits(int steps, int per) {
+  const int n = int((uint32_t(steps) + uint32_t(per) - 1) / uint32_t(per));
+  return n < 1 ? 1 : n;
+}
+
 }  // namespace skg

@@ -66,8 +66,6 @@ struct TreeArgs {
   float* ml;         // their M and l: [split][row group][head][tile][2]
 };
 
-constexpr int kStep = 32;           // keys of a step
-constexpr int kMinSteps = 8;        // steps of a split at least, where a sequence is split
 constexpr int kMaxSplitSeqs = 256;  // sequences that a launch may split
 
 __device__ inline KvSpan span_of(const TreeArgs& a, int b) {
@@ -102,13 +100,11 @@ __device__ __forceinline__ Splits lane_span(const TreeArgs& a, int b) {
   if (b < a.n_seqs) s.sp = span_of(a, b);
   return s;
 }
-__device__ inline int steps_of(const KvSpan& sp) { return sp.keys / kStep + (sp.keys % kStep != 0); }
-constexpr int kDear = 5, kCheap = 3;
+constexpr int kDear = kMaxWeight, kCheap = 3;
 __device__ inline bool dear(const TreeArgs& a, const KvSpan& sp) { return 2 * sp.n * a.group > a.tile; }
 template <bool WEIGH>
 __device__ inline int cost_of(const TreeArgs& a, const KvSpan& sp) {
-  const int each = !WEIGH ? 1 : dear(a, sp) ? kDear : kCheap;
-  return sp.n == 0 ? 0 : (unsigned(steps_of(sp) * each) + (1u << a.cost_shift) - 1) >> a.cost_shift;
+  return sp.n == 0 ? 0 : kv_cost(kv_steps(sp.keys), !WEIGH ? 1 : dear(a, sp) ? kDear : kCheap, a.cost_shift);
 }
 // Cost of a split.
 template <bool WEIGH>
@@ -125,14 +121,13 @@ __device__ __forceinline__ int split_cost(const TreeArgs& a, const Splits& first
 // Steps of a split of a sequence.
 template <bool WEIGH>
 __device__ __forceinline__ int split_steps(const TreeArgs& a, const KvSpan& sp, int cost) {
-  const unsigned most = (1u << 27) >> a.cost_shift, c = (unsigned(cost) < most ? unsigned(cost) : most) << a.cost_shift;
-  const int per = int(!WEIGH ? c : dear(a, sp) ? (c + kDear - 1) / kDear : (c + kCheap - 1) / kCheap);
-  return per < kMinSteps ? kMinSteps : per;
+  return !WEIGH          ? kv_split_steps(cost, 1, a.cost_shift)
+         : dear(a, sp) ? kv_split_steps(cost, kDear, a.cost_shift)
+                       : kv_split_steps(cost, kCheap, a.cost_shift);
 }
 template <bool WEIGH>
 __device__ __forceinline__ void count_splits(const TreeArgs& a, Splits& s, int cost, int before) {
-  const int per = split_steps<WEIGH>(a, s.sp, cost), n = (steps_of(s.sp) + per - 1) / per;
-  s.n = s.sp.n == 0 ? 0 : n < 1 ? 1 : n;
+  s.n = s.sp.n == 0 ? 0 : kv_splits(kv_steps(s.sp.keys), split_steps<WEIGH>(a, s.sp, cost));
   const int incl = a.n_seqs > 1 ? wave_scan(s.n) : s.n;
   s.incl = before + incl;
 }
@@ -150,7 +145,7 @@ __device__ __forceinline__ bool find_unit(const TreeArgs& a, int u, Unit& w, boo
     w.seq = u;
     w.sp = span_of(a, u);
     w.begin = 0;
-    w.end = steps_of(w.sp);
+    w.end = kv_steps(w.sp.keys);
     w.splits = 1;
     w.base = 0;
     return true;
@@ -172,7 +167,7 @@ __device__ __forceinline__ bool find_unit(const TreeArgs& a, int u, Unit& w, boo
       w.sp = KvSpan{lane_of(s.sp.t0, b), lane_of(s.sp.ctx, b), lane_of(s.sp.n, b), lane_of(s.sp.keys, b)};
       const int per = split_steps<WEIGH>(a, w.sp, cost);
       w.begin = (u - w.base) * per;
-      const int all = steps_of(w.sp);
+      const int all = kv_steps(w.sp.keys);
       w.end = w.begin + per < all ? w.begin + per : all;
       return true;
     }

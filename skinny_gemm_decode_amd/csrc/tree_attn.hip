@@ -210,8 +210,7 @@ hipError_t launch_tree_attn(const TreeArgs& args, int kind, int D, skg_dtype dt,
   TreeArgs a = args;
   const Plan p = plan(kind, D, heads, dt, a.T, a.n_seqs, a.hq, a.max_draft, a.max_kv);
   a.want = p.want;
-  a.cost_shift = 0;
-  while ((((a.max_kv + kStep - 1) / kStep * kDear) >> a.cost_shift) + 1 > INT32_MAX / a.n_seqs) ++a.cost_shift;
+  a.cost_shift = kv_cost_shift(a.max_kv, a.n_seqs);
   a.row_groups = p.row_groups;
   a.tile = kTileOf[p.form];
   a.per_seq = int(a.T / a.n_seqs);

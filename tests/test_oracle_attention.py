@@ -143,3 +143,61 @@ def test_cache_addresses_on_the_host(tmp_path):
                     os.path.join(ROOT, "skinny_gemm_decode_amd", "csrc"), str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+_SPLIT_MAIN = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+#include "kv_layout.h"
+using namespace skg;
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+int main() {
+  std::mt19937 rng(5);
+  const int64_t bounds[] = {0, 1, 32, 100, 5000, 131072, int64_t(1) << 26, int64_t(INT32_MAX) - 64};
+  for (int trial = 0; trial < 20000; ++trial) {
+    const int64_t max_kv = bounds[rng() % 8];
+    const int n_seqs = 1 + rng() % (trial & 1 ? 256 : 4), want = 1 + rng() % (trial & 2 ? 1024 : 3);
+    const bool weigh = trial & 4;
+    const int shift = kv_cost_shift(max_kv, n_seqs);
+    CHECK(shift >= 0 && shift < 16);
+    std::vector<int> steps(n_seqs), each(n_seqs);
+    int64_t total = 0;
+    const int kind = rng() % 3;  // all as long as they may be, any, a few long ones
+    for (int b = 0; b < n_seqs; ++b) {
+      const int64_t keys = kind == 0 ? max_kv : kind == 1 || rng() % 8 == 0 ? int64_t(rng()) % (max_kv + 1) : rng() % 5;
+      steps[b] = kv_steps(int32_t(keys < max_kv ? keys : max_kv));
+      each[b] = !weigh ? 1 : rng() % 2 ? kMaxWeight : 3;
+      total += kv_cost(steps[b], each[b], shift);
+    }
+    CHECK(total <= INT32_MAX);
+    const int cost = int(total) / want + (int(total) % want != 0);
+    int64_t splits = 0;
+    const int64_t most = (((max_kv + kStep - 1) / kStep) + kMinSteps - 1) / kMinSteps;
+    for (int b = 0; b < n_seqs; ++b) {
+      const int per = kv_split_steps(cost, each[b], shift), n = kv_splits(steps[b], per);
+      CHECK(per >= kMinSteps && n >= 1 && n <= (most < 1 ? 1 : most));
+      CHECK(int64_t(per) * n >= steps[b] && int64_t(per) * (n - 1) < (steps[b] ? steps[b] : 1));
+      CHECK(int64_t(per) * n <= INT32_MAX);  // no overflow in a split's end
+      splits += n;
+    }
+    CHECK(splits <= int64_t(want) + n_seqs);
+  }
+  std::puts("ok");
+}
+"""
+
+
+def test_splits_fit_their_workspace_on_the_host(tmp_path):
+    """At most want + n_seqs splits, whatever the lengths: the arithmetic of the
+    kernels, compiled for the CPU."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    src, exe = tmp_path / "s.cpp", tmp_path / "s"
+    src.write_text(_SPLIT_MAIN)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover", "-I",
+                    os.path.join(ROOT, "skinny_gemm_decode_amd", "csrc"), str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
